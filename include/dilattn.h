@@ -231,6 +231,95 @@ int dilattn_bwd(const void* q, const void* k, const void* v, const void* out,
                 int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * The 8-bit key/value cache and the attention over it: serving a model whose
+ * layers are this library's dilated attention (the LongNet pages describe
+ * training and whole-sequence inference only; a cached token computes the row
+ * of the operation above that belongs to its position).
+ *
+ * A cache holds pages of page_size tokens (16, 32, 64 or 128):
+ *   kc, vc : [pages][Hkv][page_size][d] codes, one byte each, e4m3 or int8;
+ *   ks, vs : [pages][Hkv] float32 scales, finite and positive.
+ * A code's value is code * scale; K and V have scales of their own. A
+ * sequence's tokens lie in the pages that its row of `table` [B][max_pages]
+ * (int32) names, position p in page table[b][p / page_size] at row
+ * p mod page_size; entries past a sequence's last token are not read. All
+ * arrays are device memory, so a captured graph follows their contents.
+ * pages * Hkv * page_size < 2^32 and max_pages * page_size < 2^31.
+ *
+ * What device memory holds is checked by the kernels: a page index that names
+ * no page, a position outside the table or a sequence outside [0, B) is
+ * skipped and raises code 4 in the device error word (dilattn_device_error).
+ *
+ * Codes come from dilattn_cache_write; it leaves no NaN code behind.
+ */
+enum dilattn_cache_format { DILATTN_CACHE_E4M3 = 0, DILATTN_CACHE_INT8 = 1 };
+
+/*
+ * Write: K and V rows (bf16, [T][Hkv][d], consecutive tokens k_stride and
+ * v_stride elements apart, multiples of 8) are quantised into their pages.
+ * Sequence b writes tokens offsets[b] .. offsets[b + 1] - 1 (int32 [B + 1],
+ * ascending) at positions start[b], start[b] + 1, ...; rows of k and v at and
+ * past offsets[B] are not read. offsets = NULL: T = B, one token for each
+ * sequence. A sequence may have no token.
+ *
+ * Scales are powers of two, one for each (page, KV head): 2^e, the least
+ * e >= -126 for which the largest magnitude written to the page and head is at most 448 * 2^e
+ * (e4m3) or 127 * 2^e (int8). Every code is value / scale rounded to nearest,
+ * ties to even. A call that writes row 0 of a page starts it afresh: its
+ * scale comes from the call's rows alone, and the page's other rows hold
+ * nothing until they are written. Otherwise the scale only grows; when it
+ * does, the page's other codes are rounded again to the new scale. A NaN or
+ * an infinity makes the scale of its page and head NaN, which every read of
+ * the page and head then gives, until row 0 is written again.
+ *
+ * One call must not write a page for two sequences. Calls that write and read
+ * one page must be ordered, e.g. on one stream.
+ */
+int dilattn_cache_write(const void* k, const void* v, long long k_stride, long long v_stride,
+                        const int* offsets, const int* start, int T, const int* table, int B,
+                        int max_pages, void* kc, void* vc, float* ks, float* vs, int pages,
+                        int Hkv, int page_size, int d, int format, cudaStream_t stream);
+
+/*
+ * Read: the tokens that offsets and start name (as in dilattn_cache_write)
+ * come back as bf16(code * scale) in k and v ([T][Hkv][d], strides as there);
+ * with the scales that dilattn_cache_write makes, no bit is lost. Rows of k
+ * and v at and past offsets[B] are left as they were; a token whose page is
+ * out of range reads as zeros.
+ */
+int dilattn_cache_read(const void* kc, const void* vc, const float* ks, const float* vs,
+                       int pages, int Hkv, int page_size, int d, int format, const int* table,
+                       int B, int max_pages, const int* offsets, const int* start, int T, void* k,
+                       void* v, long long k_stride, long long v_stride, cudaStream_t stream);
+
+/*
+ * Decode: causal merged dilated attention of single query tokens over a
+ * cache. Token i (q [T][H][d] bf16, q_stride elements apart) stands at position pos[i] of
+ * sequence seq[i] (seq = NULL: of sequence i, T <= B) and attends the cached
+ * positions up to and including pos[i] that the patterns give it: row pos[i]
+ * of dilattn_fwd on the whole sequence, for the values that the cache holds.
+ * A pattern with r = 1 and w above every position is dense attention. Query
+ * head h reads KV head h / (H / Hkv) (Hkv divides H); dilation offsets go by
+ * the query head, as if K and V were repeated to H heads. out [T][H][d] bf16;
+ * lse [T][H] float32, natural log, or NULL. pos[i] < 0 is an empty slot: like
+ * a token that no pattern keeps it gets out = 0 and lse = -inf.
+ *
+ * Scores, softmax and sums are fp32; q and the codes are exact operands, and
+ * the probabilities are rounded to 11 bits for the product with V.
+ *
+ * workspace: at least dilattn_decode_workspace_size(T, H, Hkv, d) bytes,
+ * 256-byte aligned; its contents on entry do not matter. Calls that can
+ * overlap on the GPU need workspaces of their own.
+ */
+size_t dilattn_decode_workspace_size(int T, int H, int Hkv, int d);
+int dilattn_decode(const void* q, long long q_stride, const void* kc, const void* vc,
+                   const float* ks, const float* vs, int pages, int Hkv, int page_size, int d,
+                   int format, const int* table, int B, int max_pages, const int* seq,
+                   const int* pos, void* out, float* lse, int T, int H, const int* w,
+                   const int* r, int npat, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
+/*
  * fp32 forward and backward: the same operation as dilattn_fwd / dilattn_bwd
  * (same passages), float32 tensors, no workspace, full fp32 FMA arithmetic
  * without TF32. Meant for small problems: each output row is computed by
@@ -269,7 +358,8 @@ int dilattn_set_trace_events(cudaEvent_t tile_begin, cudaEvent_t tile_end);
  * Reads and clears the library's device-side error word on the current
  * device after synchronising `stream`. *code receives 0 when no kernel
  * reported a failure, else the code of the last failure (1: a bounded wait
- * ran out). Every kernel launch carries its own tag, and its waits give up
+ * ran out; 4: a cache entry point met a page, position or sequence out of
+ * range). Every kernel launch carries its own tag, and its waits give up
  * early only on a failure of that same launch, so a failure that nobody has
  * read yet does not cut short the work of later calls; it stays readable
  * until this call clears it. The word's device address is looked up once

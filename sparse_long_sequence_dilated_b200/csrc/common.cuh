@@ -15,7 +15,8 @@ constexpr int BM = 128;   // query rows per tile (MMA M)
 constexpr int BN = 128;   // key rows per tile (MMA N of S = Q K^T)
 
 // Error codes a kernel may leave in the device error word.
-enum DevErr : int { kErrNone = 0, kErrWaitTimeout = 1, kErrBadTile = 2, kErrF16Range = 3 };
+enum DevErr : int { kErrNone = 0, kErrWaitTimeout = 1, kErrBadTile = 2, kErrF16Range = 3,
+                     kErrBadPage = 4 };
 
 // Geometry of one (w, r) pattern for a given N (host-computed, read on device).
 struct PatternGeom {

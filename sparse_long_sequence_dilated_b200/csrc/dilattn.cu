@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -19,6 +20,8 @@
 #include "fwd_tc.cuh"
 #include "bwd_tc.cuh"
 #include "simt.cuh"
+#include "cache.cuh"
+#include "decode.cuh"
 
 namespace dil {
 
@@ -299,6 +302,8 @@ int check_shape(int B, int N, int H, int d, const int* w, const int* r, int npat
 }
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
   const char* x = (const char*)a;
@@ -1057,4 +1062,272 @@ extern "C" int dilattn_fwd_noalloc(const void* q, const void* k, const void* v, 
                           stream);
   return launch_fwd<128>(q, k, v, out, nullptr, lse, B, N, H, w, r, npat, causal, scratch, st,
                          stream);
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit key/value cache and the attention over it
+// ---------------------------------------------------------------------------
+namespace dil {
+namespace {
+
+// A buffer as the overlap checks see it.
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+// The checks that every cache entry point makes of the cache and its table.
+int check_cache(const void* kc, const void* vc, const float* ks, const float* vs, int pages,
+                int Hkv, int page_size, int d, int format, const int* table, int B,
+                int max_pages) {
+  if (pages < 1 || Hkv < 1 || B < 1 || max_pages < 1) return DILATTN_ERR_INVALID_ARG;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    return DILATTN_ERR_INVALID_ARG;
+  if (format != DILATTN_CACHE_E4M3 && format != DILATTN_CACHE_INT8) return DILATTN_ERR_INVALID_ARG;
+  // cache rows are counted in 32 bits, positions in 31
+  if ((double)pages * Hkv * page_size >= 4294967295.0 ||
+      (double)max_pages * page_size > 2147483647.0)
+    return DILATTN_ERR_INVALID_ARG;
+  if (!aligned16(kc) || !aligned16(vc) || !aligned16(ks) || !aligned16(vs) || !aligned4(table))
+    return DILATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return DILATTN_ERR_UNSUPPORTED;
+  const size_t cb = (size_t)pages * Hkv * page_size * d, sb = (size_t)pages * Hkv * 4;
+  const Span s[5] = {{kc, cb}, {vc, cb}, {ks, sb}, {vs, sb}, {table, (size_t)B * max_pages * 4}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlaps(s[i].p, s[i].n, s[j].p, s[j].n)) return DILATTN_ERR_INVALID_ARG;
+  return DILATTN_OK;
+}
+
+// Bytes from the first element to the last of n rows of `row` 2-byte elements, `stride` apart.
+size_t strided_bytes(long long n, long long row, long long stride) {
+  return n < 1 ? 0 : (size_t)((n - 1) * stride + row) * 2;
+}
+
+// Whether two sets of n rows of `row` 2-byte elements share an element. Sets
+// of the same stride may interleave, as slices of one buffer do: then their
+// rows are `shift` bytes apart, modulo the stride.
+bool rows_overlap(const void* a, long long a_stride, const void* b, long long b_stride,
+                  long long n, long long row) {
+  if (!overlaps(a, strided_bytes(n, row, a_stride), b, strided_bytes(n, row, b_stride)))
+    return false;
+  if (a_stride != b_stride) return true;
+  const long long shift = std::llabs((const char*)a - (const char*)b) % (2 * a_stride);
+  return shift < 2 * row || shift > 2 * (a_stride - row);
+}
+
+// Row strides count elements: at least one row, and 16-byte aligned.
+bool good_stride(long long stride, long long row) {
+  return stride >= row && stride % 8 == 0 && stride < (1ll << 40);
+}
+
+CacheGeom cache_geom(const int* table, int B, int max_pages, int pages, int Hkv, int page_size,
+                     DeviceState* st) {
+  CacheGeom g;
+  g.table = table;
+  g.B = B;
+  g.max_pages = max_pages;
+  g.pages = pages;
+  g.Hkv = Hkv;
+  g.lp = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+  g.err = ErrCtx{st->err_word, next_tag()};
+  return g;
+}
+
+// Checks of the ragged token batch that writes and reads share.
+int check_tokens(const void* k, const void* v, long long k_stride, long long v_stride,
+                 const int* offsets, const int* start, int T, int B, int Hkv, int d) {
+  if (T < 0 || (offsets == nullptr && T != B)) return DILATTN_ERR_INVALID_ARG;
+  if (!aligned4(start) || (offsets != nullptr && !aligned4(offsets)))
+    return DILATTN_ERR_INVALID_ARG;
+  const long long row = (long long)Hkv * d;
+  if (T > 0 && (!aligned16(k) || !aligned16(v))) return DILATTN_ERR_INVALID_ARG;
+  if (!good_stride(k_stride, row) || !good_stride(v_stride, row)) return DILATTN_ERR_INVALID_ARG;
+  return DILATTN_OK;
+}
+
+// Whether a written buffer overlaps a read one.
+bool any_overlap(const Span* mut, int nm, const Span* ro, int nr) {
+  for (int i = 0; i < nm; ++i)
+    for (int j = 0; j < nr; ++j)
+      if (overlaps(mut[i].p, mut[i].n, ro[j].p, ro[j].n)) return true;
+  return false;
+}
+
+}  // namespace
+}  // namespace dil
+
+extern "C" int dilattn_cache_write(const void* k, const void* v, long long k_stride,
+                                   long long v_stride, const int* offsets, const int* start,
+                                   int T, const int* table, int B, int max_pages, void* kc,
+                                   void* vc, float* ks, float* vs, int pages, int Hkv,
+                                   int page_size, int d, int format, cudaStream_t stream) {
+  int rc = check_cache(kc, vc, ks, vs, pages, Hkv, page_size, d, format, table, B, max_pages);
+  if (rc != DILATTN_OK) return rc;
+  rc = check_tokens(k, v, k_stride, v_stride, offsets, start, T, B, Hkv, d);
+  if (rc != DILATTN_OK) return rc;
+  if (T == 0) return DILATTN_OK;
+  const size_t cb = (size_t)pages * Hkv * page_size * d, sb = (size_t)pages * Hkv * 4;
+  const long long row = (long long)Hkv * d;
+  const Span mut[4] = {{kc, cb}, {vc, cb}, {ks, sb}, {vs, sb}};
+  const Span ro[4] = {{k, strided_bytes(T, row, k_stride)},
+                      {v, strided_bytes(T, row, v_stride)},
+                      {start, (size_t)B * 4},
+                      {offsets, offsets != nullptr ? (size_t)(B + 1) * 4 : 0}};
+  if (any_overlap(mut, 4, ro, 4)) return DILATTN_ERR_INVALID_ARG;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc != DILATTN_OK) return rc;
+  NvtxRange range("dilattn cache write");
+  CacheWriteParams p;
+  p.geom = cache_geom(table, B, max_pages, pages, Hkv, page_size, st);
+  p.tok = CacheTokens{offsets, start, T};
+  p.x[0] = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.x[1] = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.stride[0] = k_stride;
+  p.stride[1] = v_stride;
+  p.codes[0] = reinterpret_cast<uint8_t*>(kc);
+  p.codes[1] = reinterpret_cast<uint8_t*>(vc);
+  p.scale[0] = ks;
+  p.scale[1] = vs;
+  const long long slots = (long long)T / page_size + 2ll * B + 1;
+  if (slots > 0x7fffffffLL || Hkv > 65535) return DILATTN_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)slots, (unsigned)Hkv, 2);
+  if (format == DILATTN_CACHE_E4M3) {
+    if (d == 64) cache_write_kernel<64, kFmtE4M3><<<grid, 128, 0, stream>>>(p);
+    else cache_write_kernel<128, kFmtE4M3><<<grid, 128, 0, stream>>>(p);
+  } else {
+    if (d == 64) cache_write_kernel<64, kFmtInt8><<<grid, 128, 0, stream>>>(p);
+    else cache_write_kernel<128, kFmtInt8><<<grid, 128, 0, stream>>>(p);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "cache_write_kernel launch");
+  return DILATTN_OK;
+}
+
+extern "C" int dilattn_cache_read(const void* kc, const void* vc, const float* ks,
+                                  const float* vs, int pages, int Hkv, int page_size, int d,
+                                  int format, const int* table, int B, int max_pages,
+                                  const int* offsets, const int* start, int T, void* k, void* v,
+                                  long long k_stride, long long v_stride, cudaStream_t stream) {
+  int rc = check_cache(kc, vc, ks, vs, pages, Hkv, page_size, d, format, table, B, max_pages);
+  if (rc != DILATTN_OK) return rc;
+  rc = check_tokens(k, v, k_stride, v_stride, offsets, start, T, B, Hkv, d);
+  if (rc != DILATTN_OK) return rc;
+  if (T == 0) return DILATTN_OK;
+  const size_t cb = (size_t)pages * Hkv * page_size * d, sb = (size_t)pages * Hkv * 4;
+  const long long row = (long long)Hkv * d;
+  if (rows_overlap(k, k_stride, v, v_stride, T, row)) return DILATTN_ERR_INVALID_ARG;
+  const Span mut[2] = {{k, strided_bytes(T, row, k_stride)}, {v, strided_bytes(T, row, v_stride)}};
+  const Span ro[7] = {{kc, cb}, {vc, cb}, {ks, sb}, {vs, sb},
+                      {table, (size_t)B * max_pages * 4}, {start, (size_t)B * 4},
+                      {offsets, offsets != nullptr ? (size_t)(B + 1) * 4 : 0}};
+  if (any_overlap(mut, 2, ro, 7)) return DILATTN_ERR_INVALID_ARG;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc != DILATTN_OK) return rc;
+  NvtxRange range("dilattn cache read");
+  CacheReadParams p;
+  p.geom = cache_geom(table, B, max_pages, pages, Hkv, page_size, st);
+  p.tok = CacheTokens{offsets, start, T};
+  p.x[0] = reinterpret_cast<__nv_bfloat16*>(k);
+  p.x[1] = reinterpret_cast<__nv_bfloat16*>(v);
+  p.stride[0] = k_stride;
+  p.stride[1] = v_stride;
+  p.codes[0] = reinterpret_cast<const uint8_t*>(kc);
+  p.codes[1] = reinterpret_cast<const uint8_t*>(vc);
+  p.scale[0] = ks;
+  p.scale[1] = vs;
+  const long long pieces = (long long)T * Hkv * (d / 16);
+  const dim3 grid((unsigned)std::min<long long>((pieces + 255) / 256, (long long)st->num_sms * 64),
+                  1, 2);
+  if (format == DILATTN_CACHE_E4M3) {
+    if (d == 64) cache_read_kernel<64, kFmtE4M3><<<grid, 256, 0, stream>>>(p);
+    else cache_read_kernel<128, kFmtE4M3><<<grid, 256, 0, stream>>>(p);
+  } else {
+    if (d == 64) cache_read_kernel<64, kFmtInt8><<<grid, 256, 0, stream>>>(p);
+    else cache_read_kernel<128, kFmtInt8><<<grid, 256, 0, stream>>>(p);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "cache_read_kernel launch");
+  return DILATTN_OK;
+}
+
+extern "C" size_t dilattn_decode_workspace_size(int T, int H, int Hkv, int d) {
+  if (T < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  return 256;
+}
+
+extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc, const void* vc,
+                              const float* ks, const float* vs, int pages, int Hkv, int page_size,
+                              int d, int format, const int* table, int B, int max_pages,
+                              const int* seq, const int* pos, void* out, float* lse, int T, int H,
+                              const int* w, const int* r, int npat, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  int rc = check_cache(kc, vc, ks, vs, pages, Hkv, page_size, d, format, table, B, max_pages);
+  if (rc != DILATTN_OK) return rc;
+  if (T < 0 || H < 1 || H % Hkv != 0 || (seq == nullptr && T > B)) return DILATTN_ERR_INVALID_ARG;
+  if (npat < 1 || npat > DILATTN_MAX_PATTERNS || w == nullptr || r == nullptr)
+    return DILATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < npat; ++i)
+    if (w[i] < 1 || r[i] < 1) return DILATTN_ERR_INVALID_ARG;
+  if (!good_stride(q_stride, (long long)H * d) || (seq != nullptr && !aligned4(seq)))
+    return DILATTN_ERR_INVALID_ARG;
+  if ((double)T * H * d >= 1099511627776.0 || (double)T * H > 2147483647.0)
+    return DILATTN_ERR_INVALID_ARG;
+  if (T == 0) return DILATTN_OK;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(pos) || (lse != nullptr && !aligned16(lse)))
+    return DILATTN_ERR_INVALID_ARG;
+  const size_t need = dilattn_decode_workspace_size(T, H, Hkv, d);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 ||
+      workspace_bytes < need)
+    return DILATTN_ERR_WORKSPACE;
+  const size_t cb = (size_t)pages * Hkv * page_size * d, sb = (size_t)pages * Hkv * 4;
+  const Span mut[3] = {{out, (size_t)T * H * d * 2},
+                       {workspace, need},
+                       {lse, lse != nullptr ? (size_t)T * H * 4 : 0}};
+  const Span ro[8] = {{kc, cb}, {vc, cb}, {ks, sb}, {vs, sb},
+                      {table, (size_t)B * max_pages * 4},
+                      {q, strided_bytes(T, (long long)H * d, q_stride)},
+                      {pos, (size_t)T * 4},
+                      {seq, seq != nullptr ? (size_t)T * 4 : 0}};
+  if (any_overlap(mut, 3, ro, 8) || any_overlap(mut, 1, mut + 1, 2) ||
+      any_overlap(mut + 1, 1, mut + 2, 1))
+    return DILATTN_ERR_INVALID_ARG;
+  DeviceState* st = nullptr;
+  rc = device_state(&st);
+  if (rc != DILATTN_OK) return rc;
+  NvtxRange range("dilattn decode");
+  DecodeParams p;
+  memset(&p, 0, sizeof(p));
+  p.geom = cache_geom(table, B, max_pages, pages, Hkv, page_size, st);
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.codes[0] = reinterpret_cast<const uint8_t*>(kc);
+  p.codes[1] = reinterpret_cast<const uint8_t*>(vc);
+  p.scale[0] = ks;
+  p.scale[1] = vs;
+  p.seq = seq;
+  p.pos = pos;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.T = T;
+  p.H = H;
+  p.qk_scale = (float)(1.4426950408889634 / std::sqrt((double)d));
+  p.npat = npat;
+  for (int i = 0; i < npat; ++i) {
+    p.w[i] = w[i];
+    p.r[i] = r[i];
+  }
+  const unsigned grid = (unsigned)(T * H);
+  if (format == DILATTN_CACHE_E4M3) {
+    if (d == 64) decode_kernel<64, kFmtE4M3><<<grid, 128, 0, stream>>>(p);
+    else decode_kernel<128, kFmtE4M3><<<grid, 128, 0, stream>>>(p);
+  } else {
+    if (d == 64) decode_kernel<64, kFmtInt8><<<grid, 128, 0, stream>>>(p);
+    else decode_kernel<128, kFmtInt8><<<grid, 128, 0, stream>>>(p);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "decode_kernel launch");
+  return DILATTN_OK;
 }

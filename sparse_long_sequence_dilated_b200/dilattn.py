@@ -3,7 +3,7 @@
 The ``dilattn_*`` functions mirror the C entry points one to one (integer
 device pointers and sizes). The torch-facing functions (``fwd``,
 ``fwd_train``, ``bwd``, ``fwd_fp8``, ``fwd_noalloc``, ``fwd_seqpar``,
-``pack_dilated``, ``selection``) add only argument marshalling for torch
+``pack_dilated``, ``selection``, ``cache_write``, ``cache_read``, ``decode``) add only argument marshalling for torch
 tensors: checks of every tensor's shape, dtype, layout and device (the C
 entry points take bare pointers and cannot see a buffer's size), output and
 workspace allocation with torch, and the current CUDA stream. Every step of the
@@ -12,9 +12,10 @@ and a missing or unloadable library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Sequence, Tuple
+from typing import Any, NamedTuple, Optional, Sequence, Tuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libdilattn.so")
@@ -26,6 +27,7 @@ _c = ctypes
 _vp = _c.c_void_p
 _i = _c.c_int
 _sz = _c.c_size_t
+_ll = _c.c_longlong
 _ip = _c.POINTER(_c.c_int)
 
 # name -> (restype, argtypes); exactly the functions include/dilattn.h declares
@@ -51,6 +53,13 @@ SIGNATURES = {
     "dilattn_fwd_seqpar": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _ip, _ip, _i, _i, _i, _i,
                                 _c.POINTER(_vp), _c.POINTER(_vp), _vp]),
     "dilattn_pack_dilated": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "dilattn_cache_write": (_i, [_vp, _vp, _ll, _ll, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp,
+                                 _i, _i, _i, _i, _i, _vp]),
+    "dilattn_cache_read": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _i,
+                                _vp, _vp, _ll, _ll, _vp]),
+    "dilattn_decode_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "dilattn_decode": (_i, [_vp, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _i, _vp, _vp,
+                            _vp, _vp, _i, _i, _ip, _ip, _i, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -386,4 +395,184 @@ def fwd_fp8(q8, k8, v, patterns, q_scale: float, k_scale: float, causal: bool = 
                                 lse.data_ptr(), B, N, H, d, w, r, n, int(causal), float(q_scale),
                                 float(k_scale), _stream_handle(stream))
     _check(rc, "dilattn_fwd_fp8")
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit key/value cache and the attention over it
+# ---------------------------------------------------------------------------
+class Cache(NamedTuple):
+    """A paged 8-bit key/value cache: the four device arrays dilattn_cache_write fills.
+
+    k, v: codes [pages, Hkv, page_size, d], float8_e4m3fn or int8;
+    k_scale, v_scale: float32 [pages, Hkv]. A code's value is code * scale."""
+    k: Any
+    v: Any
+    k_scale: Any
+    v_scale: Any
+
+
+def new_cache(pages: int, Hkv: int, page_size: int, d: int, fmt: str = "e4m3",
+              device="cuda") -> Cache:
+    """An empty cache: pages of page_size tokens, "e4m3" or "int8" codes."""
+    torch = _torch()
+    if fmt not in ("e4m3", "int8"):
+        raise ValueError(f"fmt {fmt!r}: expected 'e4m3' or 'int8'")
+    dtype = torch.float8_e4m3fn if fmt == "e4m3" else torch.int8
+    codes = [torch.zeros((pages, Hkv, page_size, d), dtype=torch.uint8, device=device).view(dtype)
+             for _ in range(2)]
+    scales = [torch.ones((pages, Hkv), dtype=torch.float32, device=device) for _ in range(2)]
+    return Cache(*codes, *scales)
+
+
+def _cache_args(cache, table):
+    """The checked arguments of a cache and its table that the C calls share:
+    (device, (kc, vc, ks, vs, pages, Hkv, page_size, d, format), (table, B, max_pages))."""
+    torch = _torch()
+    if cache.k.dim() != 4:
+        raise ValueError("expected a [pages, Hkv, page_size, d] cache")
+    pages, Hkv, P, d = (int(x) for x in cache.k.shape)
+    _need(cache.k, "cache.k", (pages, Hkv, P, d), (torch.float8_e4m3fn, torch.int8))
+    dev = cache.k.device
+    _need(cache.v, "cache.v", (pages, Hkv, P, d), (cache.k.dtype,), dev)
+    for name, t in (("cache.k_scale", cache.k_scale), ("cache.v_scale", cache.v_scale)):
+        _need(t, name, (pages, Hkv), (torch.float32,), dev)
+    if table.dim() != 2:
+        raise ValueError("expected a [B, max_pages] table")
+    _need(table, "table", tuple(table.shape), (torch.int32,), dev)
+    fmt = 0 if cache.k.dtype == torch.float8_e4m3fn else 1
+    return dev, (cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+                 cache.v_scale.data_ptr(), pages, Hkv, P, d, fmt), \
+        (table.data_ptr(), int(table.shape[0]), int(table.shape[1]))
+
+
+def _need_rows(t, name, shape, device):
+    """Raise ValueError unless t is a bf16 [T, heads, d] tensor on this device whose rows
+    are whole; returns the distance of its tokens in elements (multiples of 8 are taken)."""
+    torch = _torch()
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    row = int(shape[1]) * int(shape[2])
+    stride = int(t.stride(0)) if t.shape[0] > 1 else row
+    if t.shape[0] == 0 or not t[0].is_contiguous() or stride < row or stride % 8:
+        _need(t, name, shape, (torch.bfloat16,), device)
+        return row
+    _need(t[:1], name, (1,) + tuple(shape[1:]), (torch.bfloat16,), device)
+    return stride
+
+
+def _on(device, stream):
+    """(guard that makes the device and a given stream current, stream handle). Allocations
+    under the guard belong to that stream."""
+    torch = _torch()
+    if stream is not None and device.type == "cuda":
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        return torch.cuda.stream(stream), _stream_handle(stream)
+    if device.type != "cuda" or torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext(), _stream_handle(stream)
+    return torch.cuda.device(device), _stream_handle(torch.cuda.current_stream(device))
+
+
+def _ranges(start, offsets, T, B, dev):
+    torch = _torch()
+    _need(start, "start", (B,), (torch.int32,), dev)
+    if offsets is None:
+        if T != B:
+            raise ValueError(f"{T} tokens without offsets: expected one for each of {B} sequences")
+        return None
+    _need(offsets, "offsets", (B + 1,), (torch.int32,), dev)
+    return offsets.data_ptr()
+
+
+def cache_write(cache: Cache, k, v, table, start, offsets=None, stream=None) -> None:
+    """dilattn_cache_write: quantise K and V rows (bf16 [T, Hkv, d]; the tokens may be strided)
+    into the pages that table [B, max_pages] int32 names. Sequence b's rows are
+    offsets[b]:offsets[b + 1] (int32 [B + 1]; None: one row for each sequence) and go to positions
+    start[b], start[b] + 1, ... (int32 [B])."""
+    dev, c, (tp, B, mp) = _cache_args(cache, table)
+    Hkv, d = c[5], c[7]
+    T = int(k.shape[0]) if k.dim() == 3 else -1
+    sk = _need_rows(k, "k", (T, Hkv, d), dev)
+    sv = _need_rows(v, "v", (T, Hkv, d), dev)
+    op = _ranges(start, offsets, T, B, dev)
+    guard, s = _on(dev, stream)
+    with guard:
+        rc = load().dilattn_cache_write(k.data_ptr(), v.data_ptr(), sk, sv, op, start.data_ptr(), T,
+                                        tp, B, mp, *c, s)
+    _check(rc, "dilattn_cache_write")
+
+
+def cache_read(cache: Cache, table, start, offsets=None, total: Optional[int] = None, k=None,
+               v=None, stream=None):
+    """dilattn_cache_read: (k, v), bf16 [total, Hkv, d], of the tokens that offsets and start name
+    (as in cache_write). Rows at and past offsets[B] are left as they were."""
+    torch = _torch()
+    dev, c, (tp, B, mp) = _cache_args(cache, table)
+    Hkv, d = c[5], c[7]
+    if total is None:
+        if offsets is not None:
+            raise ValueError("offsets without total: the number of rows is not known on the host")
+        total = B
+    shape = (int(total), Hkv, d)
+    op = _ranges(start, offsets, shape[0], B, dev)
+    guard, s = _on(dev, stream)
+    with guard:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+        sk, sv = _need_rows(k, "k", shape, dev), _need_rows(v, "v", shape, dev)
+        rc = load().dilattn_cache_read(*c, tp, B, mp, op, start.data_ptr(), shape[0], k.data_ptr(),
+                                       v.data_ptr(), sk, sv, s)
+    _check(rc, "dilattn_cache_read")
+    return k, v
+
+
+def decode_workspace_size(T: int, H: int, Hkv: int, d: int) -> int:
+    return int(load().dilattn_decode_workspace_size(T, H, Hkv, d))
+
+
+def decode_workspace(T: int, H: int, Hkv: int, d: int, device="cuda"):
+    """A workspace for decode calls of up to these sizes. Calls that can overlap on the GPU
+    (other streams, graphs that replay at the same time) need one each."""
+    torch = _torch()
+    return torch.empty(max(decode_workspace_size(T, H, Hkv, d), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def decode(q, cache: Cache, table, pos, patterns, seq=None, out=None, lse=None, workspace=None,
+           stream=None):
+    """dilattn_decode: dilated attention of single query tokens (bf16 [T, H, d]) at positions
+    pos (int32 [T]; negative: an empty slot) of sequences seq (int32 [T]; None: token i belongs
+    to sequence i) over the cached positions up to and including their own.
+
+    Returns (out [T, H, d] bf16, lse [T, H] float32)."""
+    torch = _torch()
+    dev, c, (tp, B, mp) = _cache_args(cache, table)
+    Hkv, d = c[5], c[7]
+    if q.dim() != 3:
+        raise ValueError("expected a [T, H, d] q")
+    T, H = int(q.shape[0]), int(q.shape[1])
+    if H < 1 or H % Hkv:
+        raise ValueError(f"{H} query heads over {Hkv} KV heads")
+    sq = _need_rows(q, "q", (T, H, d), dev)
+    _need(pos, "pos", (T,), (torch.int32,), dev)
+    if seq is not None:
+        _need(seq, "seq", (T,), (torch.int32,), dev)
+    elif T > B:
+        raise ValueError(f"{T} tokens without seq: at most one for each of {B} sequences")
+    w, r, n = _patterns(patterns)
+    guard, s = _on(dev, stream)
+    with guard:
+        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev) if out is None else out
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev) if lse is None else lse
+        if workspace is None:
+            workspace = decode_workspace(T, H, Hkv, d, dev)
+        _need(out, "out", (T, H, d), (torch.bfloat16,), dev)
+        _need(lse, "lse", (T, H), (torch.float32,), dev)
+        _need(workspace, "workspace", (workspace.numel(),), (torch.uint8,), dev)
+        rc = load().dilattn_decode(q.data_ptr(), sq, *c, tp, B, mp,
+                                   seq.data_ptr() if seq is not None else None, pos.data_ptr(),
+                                   out.data_ptr(), lse.data_ptr(), T, H, w, r, n,
+                                   workspace.data_ptr(), workspace.numel(), s)
+    _check(rc, "dilattn_decode")
     return out, lse

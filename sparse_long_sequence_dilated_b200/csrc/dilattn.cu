@@ -1253,9 +1253,107 @@ extern "C" int dilattn_cache_read(const void* kc, const void* vc, const float* k
   return DILATTN_OK;
 }
 
+namespace dil {
+namespace {
+
+// Workspace of a decode: tile counts, their sums, and the partials of items cut
+// between blocks or warps.
+struct DecodeScratch {
+  size_t counts, sums, marks, part, warp_part;
+  size_t total() const { return counts + sums + marks + part + warp_part; }
+};
+int decode_blocks(int G) { return kDecMaxBlocks / (G <= 8 ? 1 : 2); }
+int decode_part_heads(int G) { return std::min(G, G <= 8 ? 8 : 16); }
+long long decode_items(int T, int Hkv, int G) {
+  const int heads = G <= 8 ? 8 : 16;
+  return (long long)T * Hkv * ((G + heads - 1) / heads);
+}
+DecodeScratch decode_scratch(int T, int H, int Hkv, int d) {
+  const int G = H / Hkv;
+  const size_t blocks = decode_blocks(G), part = (size_t)decode_part_heads(G) * (d + 4) * 4;
+  DecodeScratch s;
+  s.counts = align256((size_t)decode_items(T, Hkv, G) * 4);
+  s.sums = align256(kDecGroups * 8);
+  s.marks = align256(blocks * 2 * 4);
+  s.part = align256(blocks * 2 * part);
+  s.warp_part = align256(blocks * kDecWarps * part);
+  return s;
+}
+
+// A launch that may start while the kernel before it on the stream still
+// runs; the kernel itself waits for that one's end before it reads its results.
+template <typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
+                              cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr;
+  memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int NB, int FMT>
+cudaError_t launch_decode(const DecodeParams& p, int blocks, cudaStream_t stream) {
+  using Cfg = DecodeCfg<D, NB>;
+  const int groups = (p.items + p.group - 1) / p.group;
+  decode_plan_kernel<Cfg::TR, Cfg::HEADS><<<groups, kDecWarps * 32, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // opting into this much shared memory is needed once per device; it costs nothing to repeat
+  e = cudaFuncSetAttribute(decode_kernel<D, NB, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Cfg::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_overlapped(decode_kernel<D, NB, FMT>, dim3((unsigned)blocks), kDecWarps * 32,
+                        Cfg::SMEM_BYTES, stream, p);
+  if (e != cudaSuccess || blocks == 1) return e;
+  return launch_overlapped(decode_join_kernel<D, NB>, dim3((unsigned)blocks, (unsigned)p.part_heads),
+                           D, 0, stream, p, blocks);
+}
+
+// Inverse of an odd number modulo 2^32: Newton's step doubles the correct low bits.
+uint32_t odd_inverse(uint32_t x) {
+  uint32_t y = x;  // right to 3 bits
+  for (int i = 0; i < 4; ++i) y *= 2u - x * y;
+  return y;
+}
+
+// The patterns by ascending r, with the constants of their divisions.
+void decode_patterns(DecodeParams& p, const int* w, const int* r, int npat) {
+  int order[kMaxPat];
+  for (int i = 0; i < npat; ++i) order[i] = i;
+  std::stable_sort(order, order + npat, [&](int a, int b) { return r[a] < r[b]; });
+  p.npat = npat;
+  for (int i = 0; i < npat; ++i) {
+    p.w[i] = w[order[i]];
+    p.r[i] = r[order[i]];
+    divisor_magic((uint32_t)p.w[i], p.w_mul[i], p.w_sh[i]);
+    divisor_magic((uint32_t)p.r[i], p.r_mul[i], p.r_sh[i]);
+    uint32_t odd = (uint32_t)p.r[i];
+    while ((odd & 1u) == 0) {
+      odd >>= 1;
+      ++p.r_rot[i];
+    }
+    p.r_inv[i] = odd_inverse(odd);
+    p.r_lim[i] = 0xffffffffu / (uint32_t)p.r[i];
+    for (int l = 0; l < i; ++l)
+      if (p.r[i] % p.r[l] == 0) p.divisors[i] |= 1u << l;
+  }
+}
+
+}  // namespace
+}  // namespace dil
+
 extern "C" size_t dilattn_decode_workspace_size(int T, int H, int Hkv, int d) {
   if (T < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
-  return 256;
+  return decode_scratch(T, H, Hkv, d).total();
 }
 
 extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc, const void* vc,
@@ -1314,20 +1412,49 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   p.T = T;
   p.H = H;
   p.qk_scale = (float)(1.4426950408889634 / std::sqrt((double)d));
-  p.npat = npat;
-  for (int i = 0; i < npat; ++i) {
-    p.w[i] = w[i];
-    p.r[i] = r[i];
-  }
-  const unsigned grid = (unsigned)(T * H);
+  decode_patterns(p, w, r, npat);
+  p.G = H / Hkv;
+  const int nb = p.G <= 8 ? 1 : 2;
+  p.nsub = (p.G + 8 * nb - 1) / (8 * nb);
+  p.per_token = Hkv * p.nsub;
+  divisor_magic((uint32_t)p.per_token, p.pt_mul, p.pt_sh);
+  divisor_magic((uint32_t)p.nsub, p.ns_mul, p.ns_sh);
+  p.items = (int)decode_items(T, Hkv, p.G);
+  // a plan block sums a group of items, eight (one a warp) while the sums' array lasts
+  p.group = kDecWarps * ((p.items + kDecWarps * kDecGroups - 1) / (kDecWarps * kDecGroups));
+  const DecodeScratch lay = decode_scratch(T, H, Hkv, d);
+  char* wsb = reinterpret_cast<char*>(workspace);
+  p.counts = reinterpret_cast<int*>(wsb);
+  p.sums = reinterpret_cast<long long*>(wsb + lay.counts);
+  p.begun = reinterpret_cast<int*>(wsb + lay.counts + lay.sums);
+  p.unfinished = p.begun + decode_blocks(p.G);
+  p.part = reinterpret_cast<float*>(wsb + lay.counts + lay.sums + lay.marks);
+  p.warp_part = reinterpret_cast<float*>(wsb + lay.counts + lay.sums + lay.marks + lay.part);
+  p.part_heads = decode_part_heads(p.G);
+  p.part_stride = p.part_heads * (d + 4);
+  // the most rows that an item can have: no more blocks than give each warp two tiles
+  const long long longest = (long long)max_pages * page_size;
+  double rows = 0;
+  for (int i = 0; i < npat; ++i) rows += (double)std::min<long long>(w[i], longest) / r[i] + 1;
+  const double tiles = (rows / (d == 128 ? 16 : 32) + npat) * p.items;
+  int blocks = std::min(st->num_sms * (nb == 1 ? 2 : 1), decode_blocks(p.G));
+  blocks = (int)std::min<double>(blocks, tiles / (2 * kDecWarps) + 1);
+  cudaError_t e;
   if (format == DILATTN_CACHE_E4M3) {
-    if (d == 64) decode_kernel<64, kFmtE4M3><<<grid, 128, 0, stream>>>(p);
-    else decode_kernel<128, kFmtE4M3><<<grid, 128, 0, stream>>>(p);
+    if (nb == 1)
+      e = d == 64 ? launch_decode<64, 1, kFmtE4M3>(p, blocks, stream)
+                  : launch_decode<128, 1, kFmtE4M3>(p, blocks, stream);
+    else
+      e = d == 64 ? launch_decode<64, 2, kFmtE4M3>(p, blocks, stream)
+                  : launch_decode<128, 2, kFmtE4M3>(p, blocks, stream);
   } else {
-    if (d == 64) decode_kernel<64, kFmtInt8><<<grid, 128, 0, stream>>>(p);
-    else decode_kernel<128, kFmtInt8><<<grid, 128, 0, stream>>>(p);
+    if (nb == 1)
+      e = d == 64 ? launch_decode<64, 1, kFmtInt8>(p, blocks, stream)
+                  : launch_decode<128, 1, kFmtInt8>(p, blocks, stream);
+    else
+      e = d == 64 ? launch_decode<64, 2, kFmtInt8>(p, blocks, stream)
+                  : launch_decode<128, 2, kFmtInt8>(p, blocks, stream);
   }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "decode_kernel launch");
+  if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   return DILATTN_OK;
 }

@@ -52,6 +52,17 @@ def test_head_layouts(H, Hkv, pats):
     check_decode(got, want, q, pair)
 
 
+def test_the_largest_patterns():
+    """Segment lengths and dilations up to the largest int: each keeps one row of one head at most."""
+    rng = np.random.default_rng(24)
+    top = 2 ** 31 - 1
+    pair, table = filled(rng, [40], 1, 16, 64, "int8")
+    q = normal(rng, 4, 5, 64)
+    for pats in ([(top, top)], [(top, top), (top, 1)], [(1, top), (3, top - 1), (8, 2)]):
+        got, want = run(pair, table, q, [0, 1, 3, 39], pats, [0] * 4)
+        check_decode(got, want, q, pair)
+
+
 @pytest.mark.parametrize("P", [16, 32, 64, 128])
 @pytest.mark.parametrize("d", [64, 128])
 def test_every_short_length(P, d):

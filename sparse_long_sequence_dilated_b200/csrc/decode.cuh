@@ -12,23 +12,43 @@
 // head, that holds it. Where r_l divides r_j and every head of the item that
 // takes part in j takes part in l, l walks all of j's rows from s_l on, so j's
 // walk ends there; what overlap remains (r that do not divide one another) is
-// masked row by row. An item's walks, in tiles of TR rows, are its work.
+// masked row by row. An item's walks, in tiles of 32 rows, are its work.
 //
 // Split. The tiles of all items form one sequence that is cut into equal
 // contiguous ranges, one for each warp of a persistent grid, wherever the cut
-// falls: no batch shape, length or head count leaves SMs idle. An item inside
-// one range is finished by its warp; warps of a block join theirs in shared
-// memory; items cut between blocks leave partials that decode_join_kernel
-// combines in block order (no atomics: the same call gives the same bits).
+// falls: no batch shape, length or head count leaves SMs idle. Warps do not
+// wait for one another. An item inside one range is finished by its warp; an
+// item that is cut leaves partials that decode_join_kernel combines in warp
+// order (no atomics: the same call gives the same bits).
+//
+// Launches: decode_plan_kernel describes every item's walks once and cuts the
+// sequence (in one block up to kPlanThreads items; above, decode_walks_kernel
+// describes them in many), decode_kernel, decode_join_kernel.
 #pragma once
 
 #include "cache.cuh"
 
 namespace dil {
 
-constexpr int kDecWarps = 8;
-constexpr int kDecMaxBlocks = 320;  // partial slots in the workspace; two blocks on each of 148 SMs fit
-constexpr int kDecGroups = 1024;    // most groups of items that the plan sums
+constexpr int kDecWarps = 4;         // warps of a block
+constexpr int kDecMaxSms = 160;      // the workspace has partials for the warps of this many SMs
+constexpr int kDecTile = 32;         // rows of a tile
+constexpr int kPlanThreads = 1024;   // items that one plan block describes; most groups of items
+constexpr int kWalkThreads = 256;
+
+// A warp's range of the tile sequence: its first tile is tile `tile` of item `item`.
+struct __align__(16) DecodeRange {
+  int item, tile, tiles, pad;
+};
+// One walk of an item: rows base + k r, k < n. s: the segment's start (the
+// largest int when no head of the item takes part); heads: bits of those that do.
+struct __align__(16) DecodeWalk {
+  int s, n, base;
+  uint32_t heads;
+};
+struct __align__(16) DecodeHead {
+  int b, pos, tiles, pad;
+};
 
 struct DecodeParams {
   CacheGeom geom;
@@ -41,14 +61,18 @@ struct DecodeParams {
   __nv_bfloat16* out;
   float* lse;
   int T, H, G;               // G query heads to a KV head
+  int heads;                 // most heads of an item: 8 or 16
   int nsub;                  // items that a KV head's query heads make up
   int per_token;             // Hkv * nsub
   uint32_t pt_mul, ns_mul;   // reciprocals of per_token and nsub (divisor_magic)
   int pt_sh, ns_sh;
   int items;
-  int group;                 // items whose tile counts a plan block sums
+  int group;                 // items of a group, whose tiles one block sums
+  int warps;                 // warps of the grid
+  int least;                 // fewest tiles of a range
   float qk_scale;            // log2(e) / sqrt(d)
   int npat;                  // patterns, by ascending r
+  int dense;                 // one pattern with r = 1: every head takes every row of a walk
   int w[kMaxPat], r[kMaxPat];
   uint32_t w_mul[kMaxPat], r_mul[kMaxPat];
   int w_sh[kMaxPat], r_sh[kMaxPat];
@@ -56,12 +80,12 @@ struct DecodeParams {
   int r_rot[kMaxPat];
   uint32_t divisors[kMaxPat];               // earlier patterns whose r divides this one's
   // workspace
-  int* counts;               // [items] tiles
-  long long* sums;           // [kDecGroups] tiles of each group
-  int* begun;                // [blocks] item that began before the block's range, or -1
-  int* unfinished;           // [blocks] item that begins in the block's range and ends past it, or -1
-  float* part;               // [blocks][2] partials of those two
-  float* warp_part;          // [blocks][kDecWarps] partials of items that end in a warp's range
+  DecodeHead* head;          // [items]
+  DecodeWalk* walk;          // [items][npat]
+  long long* upto;           // [items] tiles of the item's group up to and including it
+  long long* sums;           // [groups] tiles of each group
+  DecodeRange* range;        // [warps + 1]
+  float* part;               // [warps][2]: an item that began before the range; one that goes on past it
   int part_heads, part_stride;  // heads and floats of a partial: sums [heads][D], (m, mv, l, -) [heads]
 };
 
@@ -77,105 +101,39 @@ template <int D_, int NB_>
 struct DecodeCfg {
   static constexpr int D = D_, NB = NB_;
   static constexpr int HEADS = 8 * NB;
-  static constexpr int TR = D == 128 ? 16 : 32;  // rows of a tile: 4 KB of codes either way
-  static constexpr int RB = TR / 16;
-  static constexpr int BLOCKS_PER_SM = NB == 1 ? 2 : 1;  // by registers: 16 heads keep 64 sums a thread
-  static constexpr int STAGES = NB == 1 ? 3 : 6;
-  static constexpr int STAGE_BYTES = 2 * TR * D + 2 * TR * 4;
-  static constexpr int RING_BYTES = kDecWarps * STAGES * STAGE_BYTES;
-  static constexpr int STATS = kDecWarps * 2 * HEADS;  // float4 each
-  static constexpr int SMEM_BYTES = RING_BYTES + STATS * 16 + kDecWarps * 3 * 4;
-  static_assert(kDecGroups * 8 + 64 <= RING_BYTES, "the group sums share the ring's memory");
-  static_assert(HEADS * D * 4 <= STAGES * STAGE_BYTES, "a warp's partial fits in its ring");
+  static constexpr int BLOCKS_PER_SM = (D == 64 ? 4 : 3) - (NB - 1);  // by registers: 128, 168 or 255 a thread
 };
 
-// What a warp knows of an item. Lane j holds pattern j's walk: rows
-// base + k r_j, k < n, in the item's tiles up to `tend`; s is its segment's start
-// and heads the item's heads (bits) that take part.
+// Where an item belongs.
 struct DecodeItem {
-  int token, b, pos, hk, h0, nh;
-  int tiles;
-  int s, base, n, tend;
-  uint32_t heads;
+  int token, hk, h0, nh;
 };
-
-template <int TR, int HEADS>
-__device__ __forceinline__ void load_item(const DecodeParams& p, int item, DecodeItem& it) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ DecodeItem item_of(const DecodeParams& p, int item) {
+  DecodeItem it;
   it.token = (int)udiv((uint32_t)item, p.pt_mul, p.pt_sh);
   const int c = item - it.token * p.per_token;
   it.hk = (int)udiv((uint32_t)c, p.ns_mul, p.ns_sh);
-  const int first = (c - it.hk * p.nsub) * HEADS;
+  const int first = (c - it.hk * p.nsub) * p.heads;
   it.h0 = it.hk * p.G + first;
-  it.nh = min(HEADS, p.G - first);
-  it.b = p.seq != nullptr ? p.seq[it.token] : it.token;
-  it.pos = p.pos[it.token];
-  if (it.pos >= 0 &&
-      ((unsigned)it.b >= (unsigned)p.geom.B || (it.pos >> p.geom.lp) >= p.geom.max_pages)) {
-    p.geom.err.raise(kErrBadPage);
-    it.pos = -1;
-  }
-  it.heads = 0;
-  it.n = 0;
-  it.s = 0;
-  it.base = 0;
-  if (lane < p.npat && it.pos >= 0) {
-    const int w = p.w[lane], r = p.r[lane];
-    const uint32_t rm = p.r_mul[lane];
-    const int rs = p.r_sh[lane];
-    it.s = (int)udiv((uint32_t)it.pos, p.w_mul[lane], p.w_sh[lane]) * w;
-    const int rel = it.pos - it.s;
-    const int steps = (int)udiv((uint32_t)rel, rm, rs);
-    const int off = rel - steps * r;
-    it.base = it.s + off;
-    it.n = steps + 1;
-    const int first_k = off - (it.h0 - (int)udiv((uint32_t)it.h0, rm, rs) * r);
-    for (uint32_t k = first_k < 0 ? first_k + r : first_k; k < (uint32_t)it.nh; k += (uint32_t)r)
-      it.heads |= 1u << k;  // k + r stays below 2^32
-  }
-  const uint32_t div = lane < p.npat ? p.divisors[lane] : 0u;
-  int limit = 0x7fffffff;
-  for (int l = 0; l + 1 < p.npat; ++l) {
-    const int sl = __shfl_sync(0xffffffffu, it.s, l);
-    const uint32_t hl = __shfl_sync(0xffffffffu, it.heads, l);
-    if ((div >> l & 1u) && (it.heads & ~hl) == 0) limit = min(limit, sl);
-  }
-  if (it.heads == 0) {
-    it.n = 0;
-  } else if (limit <= it.pos) {
-    it.n = limit > it.base
-               ? (int)udiv((uint32_t)(limit - 1 - it.base), p.r_mul[lane], p.r_sh[lane]) + 1
-               : 0;
-  }
-  it.tend = (int)(((uint32_t)it.n + TR - 1) / TR);
-#pragma unroll
-  for (int s = 1; s < kMaxPat; s <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, it.tend, s);
-    if (lane >= s) it.tend += v;
-  }
-  // an item without rows keeps one empty tile: the warp that has it writes its zeros
-  it.tiles = max(1, __shfl_sync(0xffffffffu, it.tend, p.npat - 1));
+  it.nh = min(p.heads, p.G - first);
+  return it;
 }
 
 // ---------------------------------------------------------------------------
 // PTX wrappers
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
-               : "memory");
+// Codes: read once by one lane each, so L1 keeps none of them.
+__device__ __forceinline__ uint4 load_codes16(const uint8_t* src) {
+  uint4 x;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(src));
+  return x;
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ uint2 load_codes8(const uint8_t* src) {
+  uint2 x;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(src));
+  return x;
 }
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -210,29 +168,146 @@ __device__ __forceinline__ void grid_dependency_release() {
 }
 
 // ---------------------------------------------------------------------------
-// Plan: the tile count of every item and of every group of items.
+// Plan
 // ---------------------------------------------------------------------------
-template <int TR, int HEADS>
-__global__ void __launch_bounds__(kDecWarps * 32)
-    decode_plan_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ long long s_sum[kDecWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+// Writes an item's head and walks; returns its number of tiles. One thread.
+__device__ int describe_item(const DecodeParams& p, int item) {
+  const DecodeItem it = item_of(p, item);
+  DecodeHead hd;
+  hd.b = p.seq != nullptr ? p.seq[it.token] : it.token;
+  hd.pos = p.pos[it.token];
+  hd.pad = 0;
+  if (hd.pos >= 0 &&
+      ((unsigned)hd.b >= (unsigned)p.geom.B || (hd.pos >> p.geom.lp) >= p.geom.max_pages)) {
+    p.geom.err.raise(kErrBadPage);
+    hd.pos = -1;
+  }
+  if (hd.pos < 0) hd.b = 0;
+  int start[kMaxPat], tiles = 0;
+  uint32_t in[kMaxPat];
+  for (int j = 0; j < p.npat; ++j) {
+    DecodeWalk wk{0x7fffffff, 0, 0, 0u};
+    if (hd.pos >= 0) {
+      const int r = p.r[j];
+      const int s = (int)udiv((uint32_t)hd.pos, p.w_mul[j], p.w_sh[j]) * p.w[j];
+      const int rel = hd.pos - s;
+      const int steps = (int)udiv((uint32_t)rel, p.r_mul[j], p.r_sh[j]);
+      const int off = rel - steps * r;
+      if (r == 1) {
+        wk.heads = (1u << it.nh) - 1;
+      } else {
+        const int first = off - (it.h0 - (int)udiv((uint32_t)it.h0, p.r_mul[j], p.r_sh[j]) * r);
+        for (uint32_t k = first < 0 ? first + r : first; k < (uint32_t)it.nh; k += (uint32_t)r)
+          wk.heads |= 1u << k;  // k + r stays below 2^32
+      }
+      if (wk.heads != 0) {
+        int limit = 0x7fffffff;
+        for (uint32_t d = p.divisors[j]; d != 0; d &= d - 1) {
+          const int l = __ffs(d) - 1;
+          if ((wk.heads & ~in[l]) == 0) limit = min(limit, start[l]);
+        }
+        wk.s = s;
+        wk.base = s + off;
+        wk.n = steps + 1;
+        if (limit <= hd.pos)
+          wk.n = limit > wk.base
+                     ? (int)udiv((uint32_t)(limit - 1 - wk.base), p.r_mul[j], p.r_sh[j]) + 1
+                     : 0;
+      }
+      start[j] = s;
+    }
+    in[j] = wk.heads;
+    tiles += (int)(((uint32_t)wk.n + kDecTile - 1) / kDecTile);
+    p.walk[(size_t)item * p.npat + j] = wk;
+  }
+  // an item without rows keeps one empty tile: the warp that has it writes its zeros
+  hd.tiles = max(tiles, 1);
+  p.head[item] = hd;
+  return hd.tiles;
+}
+
+// Inclusive sums over a block's threads; s_warp: one slot for each warp.
+__device__ __forceinline__ long long block_scan(long long x, long long* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, s);
+    if (lane >= s) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  long long before = lane < warp ? s_warp[lane] : 0;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) before += __shfl_xor_sync(0xffffffffu, before, s);
+  return x + before;
+}
+
+// A block for each group of items.
+__global__ void __launch_bounds__(kWalkThreads)
+    decode_walks_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ long long s_warp[2][kWalkThreads / 32];
+  __shared__ long long s_run[2];
   grid_dependency_release();
   const long long first = (long long)blockIdx.x * p.group;
   const int end = (int)min(first + p.group, (long long)p.items);
-  long long sum = 0;
-  for (int i = (int)first + warp; i < end; i += kDecWarps) {
-    DecodeItem it;
-    load_item<TR, HEADS>(p, i, it);
-    if (lane == 0) p.counts[i] = it.tiles;
-    sum += it.tiles;
+  long long run = 0;
+  for (int i = (int)first, k = 0; i < end; i += kWalkThreads, k ^= 1) {
+    const int item = i + threadIdx.x;
+    const long long x = run + block_scan(item < end ? describe_item(p, item) : 0, s_warp[k]);
+    if (item < end) p.upto[item] = x;
+    if (threadIdx.x == kWalkThreads - 1) s_run[k] = x;
+    __syncthreads();
+    run = s_run[k];
   }
-  if (lane == 0) s_sum[warp] = sum;
+  if (threadIdx.x == 0) p.sums[blockIdx.x] = run;
+}
+
+// One block. `describe`: it describes the items itself (one a thread, a group each).
+__global__ void __launch_bounds__(kPlanThreads)
+    decode_plan_kernel(const __grid_constant__ DecodeParams p, int describe) {
+  __shared__ long long s_sum[kPlanThreads];  // inclusive sums over groups
+  __shared__ long long s_warp[kPlanThreads / 32];
+  grid_dependency_release();
+  const int tid = threadIdx.x;
+  const int groups = (int)(((long long)p.items + p.group - 1) / p.group);
+  long long x = 0;
+  if (describe) {
+    if (tid < groups) x = describe_item(p, tid);
+  } else {
+    grid_dependency_wait();
+    if (tid < groups) x = p.sums[tid];
+  }
+  s_sum[tid] = block_scan(x, s_warp);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = 0;
-    for (int i = 0; i < kDecWarps; ++i) sum += s_sum[i];
-    p.sums[blockIdx.x] = sum;
+  const long long total = s_sum[groups - 1];
+  const int n = (int)min((long long)p.warps, (total + p.least - 1) / p.least);
+  const long long each = total / n, more = total - each * n;
+  for (int k = tid; k <= p.warps; k += kPlanThreads) {
+    DecodeRange rg{-1, 0, 0, 0};
+    if (k < n) {
+      const long long t0 = each * k + min((long long)k, more);
+      int a = 0, e = groups - 1;  // first group whose inclusive sum is above t0
+      while (a < e) {
+        const int m = (a + e) >> 1;
+        if (s_sum[m] > t0) e = m; else a = m + 1;
+      }
+      long long at = a > 0 ? s_sum[a - 1] : 0;
+      rg.item = a;
+      if (p.group > 1) {  // and in it the first such item
+        const int first = a * p.group;
+        int lo = first, hi = (int)min((long long)first + p.group, (long long)p.items) - 1;
+        while (lo < hi) {
+          const int m = (int)(((long long)lo + hi) >> 1);
+          if (at + p.upto[m] > t0) hi = m; else lo = m + 1;
+        }
+        if (lo > first) at += p.upto[lo - 1];
+        rg.item = lo;
+      }
+      rg.tile = (int)(t0 - at);
+      rg.tiles = (int)(each + (k < more ? 1 : 0));
+    }
+    p.range[k] = rg;
   }
 }
 
@@ -265,7 +340,7 @@ constexpr float kNoMax = -3e38f;
 constexpr float kMaxSlack = 4.f;
 constexpr float kPBias = 7.f;
 
-// Final value of one output element and its head's statistics.
+// Factor of the sums of an item's head, and its log-sum-exp.
 __device__ __forceinline__ float final_factor(float m, float mv, float l) {
   return l == 0.f ? 0.f : exp2f(mv - m - kPBias) / l;
 }
@@ -273,235 +348,199 @@ __device__ __forceinline__ float final_lse(float m, float l) {
   return l == 0.f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
 }
 
-// Partials: sums [heads][D], then (m, mv, l, unused) of each head.
-// Combines an item's partials of warps from .. last (last: the head that ends
-// it, when `ended`) into the result, or into dst.
-template <int D, int NB>
-__device__ void join_warps(const DecodeParams& p, int item, int from, int last, bool ended,
-                           const int* s_tail, const float4* s_stat, const uint8_t* smem,
-                           const float* warp_part, float* dst) {
-  using Cfg = DecodeCfg<D, NB>;
-  constexpr int HEADS = Cfg::HEADS;
-  const int token = item / p.per_token, c = item % p.per_token;
-  const int hk = c / p.nsub, first = (c % p.nsub) * HEADS;
-  const int nh = min(HEADS, p.G - first), h0 = hk * p.G + first;
-  for (int i = threadIdx.x; i < nh * D; i += kDecWarps * 32) {
-    const int hl = i / D, d = i % D;
-    float M = kNoMax, MV = kNoMax;
-    for (int k = from; k < last + (ended ? 1 : 0); ++k) {
-      if (k != last && s_tail[k] != item) continue;  // a warp without tiles
-      const float4 st = s_stat[(k * 2 + (k == last ? 0 : 1)) * HEADS + hl];
-      M = fmaxf(M, st.x);
-      MV = fmaxf(MV, st.y);
-    }
-    float L = 0.f, A = 0.f;
-    for (int k = from; k < last + (ended ? 1 : 0); ++k) {
-      if (k != last && s_tail[k] != item) continue;
-      const float4 st = s_stat[(k * 2 + (k == last ? 0 : 1)) * HEADS + hl];
-      const float* src = k == last ? warp_part + (size_t)k * p.part_stride
-                                   : reinterpret_cast<const float*>(smem + k * Cfg::STAGES * Cfg::STAGE_BYTES);
-      L += st.z * exp2f(st.x - M);
-      A += src[i] * exp2f(st.y - MV);
-    }
-    if (dst == nullptr) {
-      const size_t oi = (size_t)token * p.H + h0 + hl;
-      p.out[oi * D + d] = __float2bfloat16(L == 0.f ? 0.f : A * final_factor(M, MV, L));
-      if (d == 0 && p.lse != nullptr) p.lse[oi] = final_lse(M, L);
-    } else {
-      dst[i] = A;
-      if (d == 0) reinterpret_cast<float4*>(dst + p.part_heads * D)[hl] = make_float4(M, MV, L, 0.f);
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------
-// Main kernel. Per tile and warp: the codes of TR rows of K and V come through
-// a ring in shared memory that cp.async fills STAGES - 1 tiles ahead; every lane
-// copies just the bytes that it will hold in MMA fragments, so neither a bank
-// conflict nor a barrier stands between copy and use. S^T = K Q^T has the rows as
-// M and the heads as N: codes convert to the fp16 A operand exactly, K's
-// contraction index runs over d in whatever order the lanes hold it (Q follows).
-// O^T = V^T P^T takes V's codes of two rows interleaved by byte as its A
-// operand, and P through a register transpose.
+// Main kernel. A warp holds the codes of one tile, 32 rows of K and V, in
+// registers: every lane loads just the bytes that it needs in MMA fragments,
+// the next tile's K once this tile's scores are done and its V once the sums are,
+// so that a load has most of a tile's time to arrive and codes pass neither
+// shared memory nor a barrier. S^T = K Q^T has the rows as M and the heads as N:
+// codes convert to the fp16 A operand exactly, K's contraction index runs over d
+// in whatever order the lanes hold it (Q follows). O^T = V^T P^T takes V's codes
+// of two rows interleaved by byte as its A operand, and P through a register
+// transpose.
+//
+// Lane 4 g + c looks up row 8 c + g of the tile: the row of slot c (16-row block
+// c / 2, half c mod 2 of an MMA tile) in the fragments' row group g. HW heads
+// fill an MMA's 8 columns: with fewer than 8, Q is repeated, every lane gets the
+// scores of more than one column's worth of equal values, and each takes only
+// its share of the rows for the softmax (HW = 1, 2: its own row, 4: two rows, 8:
+// four), so that the softmax costs HW values a lane and not 8.
 //
 // V's scale enters through the exponent: p' = 2^(s + log2 vscale - mv) with its
 // own running maximum mv, so pages of any two sizes keep their precision, and
 // the softmax sum uses p = 2^(s - m) in fp32. p' is rounded to fp16 for the
 // product (2^-11 relative, below the bf16 rounding of the result).
 // ---------------------------------------------------------------------------
-template <int D, int NB, int FMT>
-__global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, NB>::BLOCKS_PER_SM))
+template <int D, int HEADS, int FMT>
+__global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>::BLOCKS_PER_SM))
     decode_kernel(const __grid_constant__ DecodeParams p) {
-  using Cfg = DecodeCfg<D, NB>;
-  constexpr int TR = Cfg::TR, RB = Cfg::RB, HEADS = Cfg::HEADS, ST = Cfg::STAGES;
-  constexpr int MT = D / 16;       // M tiles of O^T; k-steps of S
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NB = (HEADS + 7) / 8;
+  constexpr int MT = D / 16;                       // M tiles of O^T; k-steps of S
+  constexpr int HW = HEADS < 8 ? HEADS : 8;        // heads of an MMA's columns
+  constexpr int VR = HW <= 2 ? 1 : HW / 2;         // rows of a tile that a lane's softmax has
+  constexpr int VE = HW == 1 ? 1 : 2;              // heads of them, for each NB
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  float4* s_stat = reinterpret_cast<float4*>(smem + Cfg::RING_BYTES);  // [warp][head, tail][HEADS]
-  int* s_head = reinterpret_cast<int*>(s_stat + Cfg::STATS);  // [warp] item from before that ends here
-  int* s_tail = s_head + kDecWarps;                           // [warp] item that goes on past its range
-  int* s_mid = s_tail + kDecWarps;                            // [warp] that item began before its range
-  if (lane == 0) s_head[warp] = s_tail[warp] = -1;
+  const int row_l = 8 * c + g;                     // the row this lane looks up
+  const int first_slot = VR == 1 ? c : VR == 2 ? (c & 2) : 0;
+  // neighbouring warps of the sequence on different SMs: few ranges spread over all
+  const int wi = warp * (int)gridDim.x + (int)blockIdx.x;
 
   grid_dependency_wait();
-  // ---- this warp's range of the tile sequence
-  const int groups = (p.items + p.group - 1) / p.group;
-  long long* s_sum = reinterpret_cast<long long*>(smem);  // inclusive sums over groups
-  {
-    long long* s_warp = s_sum + kDecGroups;
-    long long v[4], run = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = tid * 4 + i;
-      run += k < groups ? p.sums[k] : 0;
-      v[i] = run;
-    }
-    long long x = run;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, s);
-      if (lane >= s) x += y;
-    }
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    long long before = x - run;
-    for (int i = 0; i < warp; ++i) before += s_warp[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_sum[tid * 4 + i] = before + v[i];
-    __syncthreads();
-  }
-  const long long total = s_sum[kDecGroups - 1];
-  // at least two tiles for each warp of a block that works
-  const long long want = (total + 2 * kDecWarps - 1) / (2 * kDecWarps);
-  const int nblk = (int)min((long long)gridDim.x, want);
-  const int bid = blockIdx.x;
-  long long cta0 = 0, cta1 = 0;
-  if (bid < nblk) {
-    cta0 = total * bid / nblk;
-    cta1 = total * (bid + 1) / nblk;
-  }
-  const long long t0 = cta0 + (cta1 - cta0) * warp / kDecWarps;
-  const long long t1 = cta0 + (cta1 - cta0) * (warp + 1) / kDecWarps;
-  int item0 = 0, tile0 = 0;
-  if (t0 < t1) {
-    int a = 0, e = groups - 1;  // first group whose inclusive sum is above t0
-    while (a < e) {
-      const int m = (a + e) >> 1;
-      if (s_sum[m] > t0) e = m; else a = m + 1;
-    }
-    long long at = a > 0 ? s_sum[a - 1] : 0;
-    int i = a * p.group;
-    const int end = min(i + p.group, p.items);
-    for (;; i += 32) {
-      const int cnt = i + lane < end ? p.counts[i + lane] : 0;
-      int x = cnt;
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, s);
-        if (lane >= s) x += y;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, at + x > t0);
-      if (past != 0 || i + 32 >= end) {
-        const int k = past != 0 ? __ffs(past) - 1 : 0;
-        item0 = i + k;
-        tile0 = (int)(t0 - at - __shfl_sync(0xffffffffu, x - cnt, k));
-        break;
-      }
-      at += __shfl_sync(0xffffffffu, x, 31);
-    }
-  }
-  __syncthreads();  // the ring takes the sums' place
+  const DecodeRange rg = p.range[wi];
   grid_dependency_release();
+  if (rg.tiles == 0) return;
 
-  // ---- the warp's walk
-  const uint32_t ring = smem_u32(smem) + warp * ST * Cfg::STAGE_BYTES;
-  const uint8_t* ring_p = smem + warp * ST * Cfg::STAGE_BYTES;
-  float* wpart = p.warp_part + ((size_t)bid * kDecWarps + warp) * p.part_stride;
-  const int row_l = TR == 16 ? (lane & 15) : lane;  // the row this lane looks up
-  DecodeItem ahead, it;      // items of the tile to fetch next and of the tile in hand
-  int a_item = item0, a_tile = tile0;
-  long long a_left = t1 - t0;
-  int f_page = -1, f_x = 0, f_hk = 0;  // looked-up page of the tile to copy next
-  bool f_some = false;
-  if (a_left > 0) load_item<TR, HEADS>(p, a_item, ahead);
+  const int pmask = (1 << p.geom.lp) - 1;
 
+  // ---- the walk to fetch from (a_...), the looked-up tile (f_...), the tile in registers
+  DecodeWalk aw;             // lane j: pattern j's walk of the item
+  int a_item = rg.item, a_left = rg.tiles, a_pos, a_hk, a_j, a_n, a_base, a_r;
+  uint32_t a_k, a_in;        // a_in: patterns of the item's head (HEADS = 1)
+  const int* a_table;
+  int f_page = -1, f_x = 0, f_hk = 0;
+  uint32_t f_meta = 0;
+  bool f_some = false, f_whole = false;
+
+  auto set_walk = [&](int j) {
+    a_j = j;
+    a_n = __shfl_sync(0xffffffffu, aw.n, j);
+    a_base = __shfl_sync(0xffffffffu, aw.base, j);
+    a_r = p.r[j];
+  };
+  auto load_walks = [&](int item) {
+    aw = DecodeWalk{0x7fffffff, 0, 0, 0u};
+    if (lane < p.npat) aw = p.walk[(size_t)item * p.npat + lane];
+    const DecodeHead hd = p.head[item];
+    a_pos = hd.pos;
+    a_table = p.geom.table + (size_t)hd.b * p.geom.max_pages;
+    const DecodeItem it = item_of(p, item);
+    a_hk = it.hk;
+    a_in = __ballot_sync(0xffffffffu, aw.heads & 1u);
+  };
   // look up the pages of the next tile's rows
   auto look_up = [&]() {
     f_some = a_left > 0;
     if (!f_some) return;
-    const int j = __popc(__ballot_sync(0xffffffffu, lane < p.npat && a_tile >= ahead.tend));
-    const int jj = min(j, p.npat - 1);
-    const int tstart = jj > 0 ? __shfl_sync(0xffffffffu, ahead.tend, jj - 1) : 0;
-    const int n = j < p.npat ? __shfl_sync(0xffffffffu, ahead.n, jj) : 0;
-    const int base = __shfl_sync(0xffffffffu, ahead.base, jj);
-    const uint32_t k = (uint32_t)(a_tile - tstart) * TR + row_l;  // may pass 2^31 in the last tile
+    const uint32_t k = a_k + row_l, n = (uint32_t)a_n;  // k may pass 2^31 in the last tile
+    f_hk = a_hk;
     f_page = -1;
-    f_hk = ahead.hk;
-    if (k < (uint32_t)n) {
-      f_x = base + (int)k * p.r[jj];
-      f_page = p.geom.table[(size_t)ahead.b * p.geom.max_pages + (f_x >> p.geom.lp)];
-      if ((unsigned)f_page >= (unsigned)p.geom.pages) {
-        p.geom.err.raise(kErrBadPage);
-        f_page = -1;
+    f_meta = 0;
+    const int x0 = (int)((uint32_t)a_base + a_k * (uint32_t)a_r);
+    f_whole = a_r == 1 && a_k + kDecTile <= n && (x0 & pmask) + kDecTile <= pmask + 1;
+    if (k < n) {
+      f_x = x0 + row_l * a_r;
+      f_page = a_table[f_x >> p.geom.lp];
+    }
+    if (p.dense) {
+      f_meta = k < n ? 0x10001u : 0u;
+    } else {
+      // patterns that hold the row: low half; the one that walks it and all before: high half
+      const int last = (int)((uint32_t)a_base + min(a_k + kDecTile - 1, n - 1) * (uint32_t)a_r);
+      uint32_t held = 1u << a_j;
+      for (int i = 0; i < p.npat; ++i) {
+        const int si = __shfl_sync(0xffffffffu, aw.s, i);
+        if (i == a_j || last < si) continue;
+        if (f_x >= si && divides(p, i, a_pos - f_x)) held |= 1u << i;
+      }
+      const uint32_t upto = (2u << a_j) - 1;
+      if constexpr (HEADS == 1) {  // how often the row counts
+        const uint32_t u = held & a_in;
+        f_meta = k < n && (u & upto) == (1u << a_j) ? __popc(u) : 0;
+      } else {
+        f_meta = k < n ? held | upto << 16 : 0u;
       }
     }
     --a_left;
-    if (++a_tile == ahead.tiles && a_left > 0) {
-      a_tile = 0;
-      load_item<TR, HEADS>(p, ++a_item, ahead);
+    a_k += kDecTile;
+    if (a_k >= n) {
+      a_k = 0;
+      const uint32_t more = __ballot_sync(0xffffffffu, aw.n > 0) & ~((2u << a_j) - 1);
+      if (more != 0) {
+        set_walk(__ffs(more) - 1);
+      } else if (a_left > 0) {
+        load_walks(++a_item);
+        const uint32_t any = __ballot_sync(0xffffffffu, aw.n > 0);
+        set_walk(any != 0 ? __ffs(any) - 1 : 0);
+      }
     }
   };
-  // copy the looked-up tile into ring stage st
-  auto copy = [&](int st) {
-    if (f_some) {
-      const uint32_t blk = (uint32_t)f_page * (uint32_t)p.geom.Hkv + (uint32_t)f_hk;
-      const bool in = f_page >= 0;
-      const uint32_t idx = in ? (blk << p.geom.lp) + (uint32_t)(f_x & ((1 << p.geom.lp) - 1)) : 0xffffffffu;
-      const uint32_t dst = ring + st * Cfg::STAGE_BYTES;
-      const uint32_t sc = dst + 2 * TR * D;
-      const size_t so = in ? blk : 0;
-      if constexpr (TR == 16) {
-        cp_async4(sc + lane * 4, p.scale[lane >> 4] + so, in);
-      } else {
-        cp_async4(sc + lane * 4, p.scale[0] + so, in);
-        cp_async4(sc + 128 + lane * 4, p.scale[1] + so, in);
-      }
+  constexpr int KQ = D / 64, VW = D / 32;  // 16-byte pieces of a K row, words of a V row, that a lane holds
+  const uint8_t* const base_k = p.codes[0] + c * 16;
+  const uint8_t* const base_v = p.codes[1] + g * (D / 8);
+  uint32_t row = 0, meta_l = 0;  // this lane's row of the cache, and what f_meta said of it
+  float ks_l = 0.f, vs_l = 0.f;
+  bool whole = false, any = false;
+  uint4 kr[4][KQ];
+  uint32_t vr[8][VW];
+  // take the looked-up tile: its rows' places and scales
+  auto resolve = [&]() {
+    bool in = f_meta != 0;
+    if (in && (unsigned)f_page >= (unsigned)p.geom.pages) {
+      p.geom.err.raise(kErrBadPage);
+      in = false;
+    }
+    const uint32_t blk = in ? (uint32_t)f_page * (uint32_t)p.geom.Hkv + (uint32_t)f_hk : 0u;
+    ks_l = p.scale[0][blk];
+    vs_l = p.scale[1][blk];
+    meta_l = in ? f_meta : 0u;
+    row = in ? (blk << p.geom.lp) + (uint32_t)(f_x & pmask) : 0u;
+    const uint32_t ins = __ballot_sync(0xffffffffu, in);
+    any = ins != 0;
+    whole = f_whole && ins == 0xffffffffu;
+    // a row that does not count stands for one that does: its codes are finite
+    const uint32_t other = __shfl_sync(0xffffffffu, row, any ? __ffs(ins) - 1 : 0);
+    if (whole) row -= (uint32_t)row_l;  // the tile's first row
+    else if (!in) row = other;
+  };
+  auto load_k = [&]() {
+    if (whole) {
+      const uint8_t* src = base_k + (size_t)(row + (uint32_t)g) * D;
 #pragma unroll
-      for (int i = 0; i < 2 * RB; ++i) {  // K rows g, g + 8 (, g + 16, g + 24)
-        const uint32_t x = __shfl_sync(0xffffffffu, idx, i * 8 + g);
-        const bool ok = x != 0xffffffffu;
-        const uint8_t* src = p.codes[0] + (ok ? (size_t)x * D : 0) + c * 16;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int q = 0; q < D / 64; ++q)
-          cp_async16(dst + (i * (D / 64) + q) * 512 + lane * 16, src + q * 64, ok);
-      }
-      const uint32_t dv = dst + TR * D;
+        for (int q = 0; q < KQ; ++q) kr[i][q] = load_codes16(src + i * 8 * D + q * 64);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 4 * RB; ++i) {  // V rows 2c, 2c + 1, 2c + 8, 2c + 9 of each 16
-        const int row = (i >> 2) * 16 + ((i >> 1) & 1) * 8 + 2 * c + (i & 1);
-        const uint32_t x = __shfl_sync(0xffffffffu, idx, row);
-        const bool ok = x != 0xffffffffu;
-        const uint8_t* src = p.codes[1] + (ok ? (size_t)x * D : 0) + g * (D / 8);
-        if constexpr (D == 128) cp_async16(dv + i * 512 + lane * 16, src, ok);
-        else cp_async8(dv + i * 256 + lane * 8, src, ok);
+      for (int i = 0; i < 4; ++i) {  // rows of slot i, row group g
+        const uint8_t* src = base_k + (size_t)__shfl_sync(0xffffffffu, row, (lane & 28) | i) * D;
+#pragma unroll
+        for (int q = 0; q < KQ; ++q) kr[i][q] = load_codes16(src + q * 64);
       }
     }
-    cp_async_commit();
+  };
+  auto load_v = [&]() {
+    const uint8_t* first = base_v + (size_t)(row + 2u * (uint32_t)c) * D;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // rows of slot i / 2, row groups 2 c and 2 c + 1
+      const uint8_t* src = first + (i >> 1) * 8 * D + (i & 1) * D;
+      if (!whole) src = base_v + (size_t)__shfl_sync(0xffffffffu, row, 8 * c + 4 * (i & 1) + (i >> 1)) * D;
+      if constexpr (D == 128) {
+        const uint4 u = load_codes16(src);
+        vr[i][0] = u.x, vr[i][1] = u.y, vr[i][2] = u.z, vr[i][3] = u.w;
+      } else {
+        const uint2 u = load_codes8(src);
+        vr[i][0] = u.x, vr[i][1] = u.y;
+      }
+    }
   };
 
+  // ---- the item in hand
+  DecodeItem it;
+  int tiles;                 // its tiles from here on
   float acc[MT][NB][4];
-  float m[2 * NB], mv[2 * NB], l[2 * NB], fac[2 * NB];
+  float m[2 * NB], mv[2 * NB], l[2 * NB], fac[2 * NB];  // of columns nb * 8 + 2 c + e
   uint32_t qf[NB][MT][2];
-  uint32_t in_pat[2 * NB];  // patterns that each of the lane's heads takes part in
-  // heads of this lane: nb * 8 + 2 c + e
+  uint32_t in_pat[2 * NB];   // patterns that each of the lane's heads takes part in
   auto begin_item = [&](int item) {
-    load_item<TR, HEADS>(p, item, it);
+    it = item_of(p, item);
+    tiles = p.head[item].tiles;
+    const uint32_t heads = lane < p.npat ? p.walk[(size_t)item * p.npat + lane].heads : 0u;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      // q of head nb * 8 + g, lifted by a power of two to [2^13, 2^14): exact in fp16
+      // q of head nb * 8 + g mod HW, lifted by a power of two to [2^13, 2^14): exact in fp16
       // (elements under 2^-37 of the largest are cut)
-      const int hl = nb * 8 + g;
+      const int hl = nb * 8 + (g & (HW - 1));
       uint2 raw[MT];
       uint32_t big = 0;
 #pragma unroll
@@ -510,6 +549,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, NB>::BLOCKS_PER_
         raw[k] = hl < it.nh ? *reinterpret_cast<const uint2*>(p.q + (long long)it.token * p.q_stride +
                                                               (it.h0 + hl) * D + d0)
                             : make_uint2(0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < MT; ++k) {
         big = max(max(big, raw[k].x & 0x7fffu), (raw[k].x >> 16) & 0x7fffu);
         big = max(max(big, raw[k].y & 0x7fffu), (raw[k].y >> 16) & 0x7fffu);
       }
@@ -539,10 +581,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, NB>::BLOCKS_PER_
         l[2 * nb + e2] = 0.f;
         in_pat[2 * nb + e2] = 0;
       }
+      if constexpr (HEADS > 1) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t b = __ballot_sync(0xffffffffu, it.heads >> (nb * 8 + k) & 1u);
-        if ((k >> 1) == c) in_pat[2 * nb + (k & 1)] = b;
+        for (int k = 0; k < HW; ++k) {
+          const uint32_t b = __ballot_sync(0xffffffffu, heads >> (nb * 8 + k) & 1u);
+          if (((2 * c) & (HW - 1)) == (k & ~1)) in_pat[2 * nb + (k & 1)] = b;
+        }
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -554,21 +598,21 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, NB>::BLOCKS_PER_
   // where a lane's sums of one of its heads lie: d = g (D / 8) + 0 .. D / 8 - 1
   auto sum_of = [&](int nb, int e, int k) { return acc[k >> 1][nb][(k & 1) * 2 + e]; };
 
-  // the item is done here or goes on elsewhere; `whole`: this warp had all of it
-  auto end_item = [&](int item, bool whole, bool ends) {
+  // The item is done here (dst null: this warp had all of it), or a partial of it goes to dst.
+  auto end_item = [&](float* dst) {
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
+#pragma unroll
+      for (int s = HW <= 2 ? 1 : HW == 4 ? 2 : 4; s < 32; s <<= 1)
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
     }
-    if (whole) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = 2 * nb + e, hl = nb * 8 + 2 * c + e;
-          if (hl >= it.nh) continue;
+      for (int e = 0; e < VE; ++e) {
+        const int i = 2 * nb + e, hl = nb * 8 + 2 * c + e;
+        if (hl >= it.nh) continue;
+        if (dst == nullptr) {
           const float f = final_factor(m[i], mv[i], l[i]);
           const size_t oi = (size_t)it.token * p.H + it.h0 + hl;
           uint32_t o[D / 16];
@@ -579,290 +623,375 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, NB>::BLOCKS_PER_
                 : __floats2bfloat162_rn(sum_of(nb, e, 2 * k) * f, sum_of(nb, e, 2 * k + 1) * f);
             o[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          uint4* dst = reinterpret_cast<uint4*>(p.out + oi * D + g * (D / 8));
+          uint4* to = reinterpret_cast<uint4*>(p.out + oi * D + g * (D / 8));
 #pragma unroll
           for (int k = 0; k < D / 64; ++k)
-            dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           if (g == 0 && p.lse != nullptr) p.lse[oi] = final_lse(m[i], l[i]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            *reinterpret_cast<float4*>(dst + hl * D + g * (D / 8) + 4 * k) =
+                make_float4(sum_of(nb, e, 4 * k), sum_of(nb, e, 4 * k + 1), sum_of(nb, e, 4 * k + 2),
+                            sum_of(nb, e, 4 * k + 3));
+          if (g == 0)
+            *reinterpret_cast<float4*>(dst + p.part_heads * D + hl * 4) = make_float4(m[i], mv[i], l[i], 0.f);
         }
-      return;
-    }
-    // a tail stays in the warp's part of the ring, a head goes to the workspace
-    if (!ends) {
-      cp_async_wait<0>();
-      __syncwarp();
-    }
-    float* dst = ends ? wpart : reinterpret_cast<float*>(smem + warp * ST * Cfg::STAGE_BYTES);
-    float4* stat = s_stat + (warp * 2 + (ends ? 0 : 1)) * HEADS;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * nb + e, hl = nb * 8 + 2 * c + e;
-        if (hl >= it.nh) continue;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          *reinterpret_cast<float4*>(dst + hl * D + g * (D / 8) + 4 * k) =
-              make_float4(sum_of(nb, e, 4 * k), sum_of(nb, e, 4 * k + 1), sum_of(nb, e, 4 * k + 2),
-                          sum_of(nb, e, 4 * k + 3));
-        if (g == 0) stat[hl] = make_float4(m[i], mv[i], l[i], 0.f);
       }
-    if (lane == 0) (ends ? s_head : s_tail)[warp] = item;
   };
 
-  if (t0 < t1) {
-    look_up();
+  // ---- start: the walk that the first tile belongs to
+  load_walks(a_item);
+  {
+    uint32_t end = ((uint32_t)aw.n + kDecTile - 1) / kDecTile;
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s) {
-      copy(s);
+    for (int s = 1; s < kMaxPat; s <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, end, s);
+      if (lane >= s) end += y;
+    }
+    const int j = min(__popc(__ballot_sync(0xffffffffu, lane < p.npat && (uint32_t)rg.tile >= end)), p.npat - 1);
+    const uint32_t before = j > 0 ? __shfl_sync(0xffffffffu, end, j - 1) : 0u;
+    set_walk(j);
+    a_k = ((uint32_t)rg.tile - before) * kDecTile;
+  }
+  look_up();
+  resolve();
+  load_k();
+  load_v();
+  look_up();
+  int item = rg.item;
+  bool from_start = rg.tile == 0;
+  begin_item(item);
+  tiles -= rg.tile;
+  float* const part = p.part + (size_t)wi * 2 * p.part_stride;
+  for (int left = rg.tiles; left > 0; --left) {
+    // ---- scores: block rb's rows g and g + 8, columns nb * 8 + 2 c and + 1
+    float sc[2][NB][4];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[rb][nb][k] = 0.f;
+#pragma unroll
+    for (int q = 0; q < KQ; ++q)
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) {
+        const uint4 ka = kr[2 * rb][q], kb = kr[2 * rb + 1][q];
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_half<FMT>(wa[k], a0, a2);
+          codes_to_half<FMT>(wb[k], a1, a3);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            mma_16816(sc[rb][nb], a0, a1, a2, a3, qf[nb][q * 4 + k][0], qf[nb][q * 4 + k][1]);
+        }
+      }
+    // ---- what the softmax needs of the lane's rows (slots first_slot ..); then the next tile
+    float ks[VR], lv[VR];
+    uint32_t meta[VR];
+    const bool some = any;
+    {
+      const float lv_l = fast_log2(vs_l);
+#pragma unroll
+      for (int v = 0; v < VR; ++v) {
+        ks[v] = ks_l, lv[v] = lv_l, meta[v] = meta_l;
+        const int from = (lane & 28) | (first_slot + v);
+        if (VR > 1 && !whole) {
+          ks[v] = __shfl_sync(0xffffffffu, ks_l, from);
+          lv[v] = __shfl_sync(0xffffffffu, lv_l, from);
+        }
+        if (VR > 1 && !(whole && p.dense)) meta[v] = __shfl_sync(0xffffffffu, meta_l, from);
+      }
+    }
+    if (left > 1) {
+      resolve();
+      load_k();
       look_up();
     }
-    int item = item0, tile = tile0, st = 0;
-    bool from_start = tile0 == 0;
-    begin_item(item);
-    for (long long left = t1 - t0; left > 0; --left) {
-      cp_async_wait<ST - 2>();
-      __syncwarp();
-      {
-        int nx = st + ST - 1;
-        if (nx >= ST) nx -= ST;
-        copy(nx);
-        look_up();
-      }
-      const uint8_t* kp = ring_p + st * Cfg::STAGE_BYTES;
-      const uint8_t* vp = kp + TR * D;
-      const float* sp = reinterpret_cast<const float*>(vp + TR * D);
-
-      // ---- which rows count, and how often
-      const int j = __popc(__ballot_sync(0xffffffffu, lane < p.npat && tile >= it.tend));
-      uint32_t held = 1;  // patterns that hold this lane's row
-      if (p.npat > 1) {
-        const int jj = min(j, p.npat - 1);
-        const int tstart = jj > 0 ? __shfl_sync(0xffffffffu, it.tend, jj - 1) : 0;
-        // rows past the walk's end wrap or lie past the token: they have no scale
-        const int x = (int)((uint32_t)__shfl_sync(0xffffffffu, it.base, jj) +
-                            (uint32_t)((tile - tstart) * TR + row_l) * (uint32_t)p.r[jj]);
-        const int dist = (int)((uint32_t)it.pos - (uint32_t)x);
-        held = 0;
-        for (int i = 0; i < p.npat; ++i) {
-          const int si = __shfl_sync(0xffffffffu, it.s, i);
-          if (x >= si && divides(p, i, dist)) held |= 1u << i;
-        }
-      }
-      const uint32_t upto = (2u << j) - 1, mine = 1u << j;
-
+    // ---- softmax weights
+    float s1[VR][NB][VE], s2[VR][NB][VE], cnt[VR][NB][VE];
+    bool raise = false;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        // ---- scores: rows rb * 16 + g and + 8, heads nb * 8 + 2 c and + 1
-        float sc[NB][4];
+    for (int v = 0; v < VR; ++v) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sc[nb][k] = 0.f;
-#pragma unroll
-        for (int q = 0; q < D / 64; ++q) {
-          const uint4 ka = *reinterpret_cast<const uint4*>(kp + ((2 * rb) * (D / 64) + q) * 512 + lane * 16);
-          const uint4 kb = *reinterpret_cast<const uint4*>(kp + ((2 * rb + 1) * (D / 64) + q) * 512 + lane * 16);
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t a0, a1, a2, a3;
-            codes_to_half<FMT>(wa[k], a0, a2);
-            codes_to_half<FMT>(wb[k], a1, a3);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma_16816(sc[nb], a0, a1, a2, a3, qf[nb][q * 4 + k][0], qf[nb][q * 4 + k][1]);
-          }
-        }
-        // ---- softmax weights
-        float cnt[NB][4], sv[NB][4];
-        bool raise = false;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {  // row half
-          const int row = rb * 16 + hf * 8 + g;
-          const float ks = sp[row];
-          const float lv = fast_log2(sp[TR + row]);
-          const uint32_t hr = __shfl_sync(0xffffffffu, held, row);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int k = hf * 2 + e, i = 2 * nb + e;
-              const uint32_t u = hr & in_pat[i];
-              // rows that are not there were filled with zeros: no scale is zero
-              const bool ok = (u & upto) == mine && ks != 0.f;
-              cnt[nb][k] = (float)__popc(u);
-              const float s = ok ? sc[nb][k] * (fac[i] * ks) : -INFINITY;
-              sc[nb][k] = s;
-              sv[nb][k] = ok ? s + lv : -INFINITY;
-              raise = raise || s > m[i] + kMaxSlack || sv[nb][k] > mv[i] + kMaxSlack;
-            }
-        }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = 2 * nb + e;
-              float a = fmaxf(sc[nb][e], sc[nb][2 + e]), b = fmaxf(sv[nb][e], sv[nb][2 + e]);
-#pragma unroll
-              for (int s = 4; s < 32; s <<= 1) {
-                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
-                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, s));
-              }
-              a = fmaxf(a, m[i]);
-              b = fmaxf(b, mv[i]);
-              l[i] *= fast_exp2(m[i] - a);
-              const float f = fast_exp2(mv[i] - b);
-              m[i] = a;
-              mv[i] = b;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                acc[mt][nb][e] *= f;
-                acc[mt][nb][2 + e] *= f;
-              }
-            }
-        }
-        uint32_t pf[NB][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float pv[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int k = hf * 2 + e, i = 2 * nb + e;
-              l[i] += fast_exp2(sc[nb][k] - m[i]) * cnt[nb][k];
-              pv[e] = fast_exp2(sv[nb][k] - (mv[i] - kPBias)) * cnt[nb][k];
-            }
-            const __half2 h2 = __floats2half2_rn(pv[0], pv[1]);
-            pf[nb][hf] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h2));
-          }
-        // ---- O^T += V^T P^T
-        constexpr int VW = D / 32;  // 32-bit words of a row that a lane holds
-        uint32_t vr[4][VW];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(vp + (rb * 4 + i) * 512 + lane * 16);
-            vr[i][0] = u.x, vr[i][1] = u.y, vr[i][2] = u.z, vr[i][3] = u.w;
+        for (int e = 0; e < VE; ++e) {
+          const int i = 2 * nb + e;
+          float x;
+          if constexpr (VR == 1) {
+            const float x0 = c & 1 ? sc[0][nb][2 + e] : sc[0][nb][e];
+            const float x1 = c & 1 ? sc[1][nb][2 + e] : sc[1][nb][e];
+            x = c & 2 ? x1 : x0;
+          } else if constexpr (VR == 2) {
+            x = c & 2 ? sc[1][nb][2 * v + e] : sc[0][nb][2 * v + e];
           } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(vp + (rb * 4 + i) * 256 + lane * 8);
-            vr[i][0] = u.x, vr[i][1] = u.y;
+            x = sc[v >> 1][nb][(v & 1) * 2 + e];
+          }
+          bool ok = meta[v] != 0;
+          cnt[v][nb][e] = 1.f;
+          if constexpr (HEADS == 1) {
+            cnt[v][nb][e] = (float)(meta[v] & 31u);
+          } else if (!p.dense) {
+            const uint32_t u = meta[v] & in_pat[i], upto = meta[v] >> 16;
+            ok = ok && (u & upto) == (upto ^ (upto >> 1));
+            cnt[v][nb][e] = (float)__popc(u);
+          }
+          const float s = ok ? x * (fac[i] * ks[v]) : -INFINITY;
+          const float t = ok ? s + lv[v] : -INFINITY;
+          s1[v][nb][e] = s;
+          s2[v][nb][e] = t;
+          raise = raise || s > m[i] + kMaxSlack || t > mv[i] + kMaxSlack;
+        }
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int i = 2 * nb + e;
+          float a = s1[0][nb][e], b = s2[0][nb][e];
+#pragma unroll
+          for (int v = 1; v < VR; ++v) {
+            a = fmaxf(a, s1[v][nb][e]);
+            b = fmaxf(b, s2[v][nb][e]);
+          }
+#pragma unroll
+          for (int s = HW <= 2 ? 1 : HW == 4 ? 2 : 4; s < 32; s <<= 1) {
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, s));
+          }
+          a = fmaxf(a, m[i]);
+          b = fmaxf(b, mv[i]);
+          l[i] *= fast_exp2(m[i] - a);
+          const float f = fast_exp2(mv[i] - b);
+          m[i] = a;
+          mv[i] = b;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            acc[mt][nb][e] *= f;
+            acc[mt][nb][2 + e] *= f;
           }
         }
+    }
+    uint32_t pf[2][NB][2];  // P^T fragments of block rb
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      uint32_t tr[VR];
+#pragma unroll
+      for (int v = 0; v < VR; ++v) {
+        float pv[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int i = 2 * nb + e;
+          l[i] += fast_exp2(s1[v][nb][e] - m[i]) * cnt[v][nb][e];
+          pv[e] = fast_exp2(s2[v][nb][e] - (mv[i] - kPBias)) * cnt[v][nb][e];
+        }
+        const __half2 h2 = __floats2half2_rn(pv[0], pv[1]);
+        tr[v] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h2));
+      }
+      // the transpose has column 2 c + e of lane group c in row group 2 c + e: the heads of
+      // other slots go to row groups 0 .. HW - 1; the columns past them are not used
+      if constexpr (VR == 1) {
+        pf[0][nb][0] = tr[0];
+        pf[0][nb][1] = __shfl_xor_sync(0xffffffffu, tr[0], 8);
+        pf[1][nb][0] = __shfl_xor_sync(0xffffffffu, tr[0], 16);
+        pf[1][nb][1] = __shfl_xor_sync(0xffffffffu, tr[0], 24);
+      } else if constexpr (VR == 2) {
+        pf[0][nb][0] = tr[0];
+        pf[0][nb][1] = tr[1];
+        pf[1][nb][0] = __shfl_xor_sync(0xffffffffu, tr[0], 16);
+        pf[1][nb][1] = __shfl_xor_sync(0xffffffffu, tr[1], 16);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) pf[v >> 1][nb][v & 1] = tr[v];
+      }
+    }
+    // ---- O^T += V^T P^T
+    if (some) {
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
         for (int k = 0; k < VW; ++k)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const uint32_t sel = half ? 0x7362 : 0x5140;
             uint32_t a0, a1, a2, a3;
-            codes_to_half<FMT>(__byte_perm(vr[0][k], vr[1][k], sel), a0, a1);
-            codes_to_half<FMT>(__byte_perm(vr[2][k], vr[3][k], sel), a2, a3);
+            codes_to_half<FMT>(__byte_perm(vr[rb * 4][k], vr[rb * 4 + 1][k], sel), a0, a1);
+            codes_to_half<FMT>(__byte_perm(vr[rb * 4 + 2][k], vr[rb * 4 + 3][k], sel), a2, a3);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
-              mma_16816(acc[2 * k + half][nb], a0, a1, a2, a3, pf[nb][0], pf[nb][1]);
+              mma_16816(acc[2 * k + half][nb], a0, a1, a2, a3, pf[rb][nb][0], pf[rb][nb][1]);
           }
-      }
-      if (++st == ST) st = 0;
-      const bool ends = ++tile == it.tiles;
-      if (ends || left == 1) {
-        if (lane == 0) s_mid[warp] = !from_start;
-        end_item(item, ends && from_start, ends);
-        if (left > 1) {
-          tile = 0;
-          from_start = true;
-          begin_item(++item);
-        }
+    }
+    if (left > 1) load_v();
+    if (--tiles == 0 || left == 1) {
+      end_item(!from_start ? part : tiles > 0 ? part + p.part_stride : nullptr);
+      if (left > 1) {
+        from_start = true;
+        begin_item(++item);
       }
     }
-  }
-
-  // ---- join the block's warps. A run is an item's partials of successive
-  // warps: tails, and the head that ends it unless it goes on in the next block.
-  __syncthreads();
-  int run = -1, from = 0, begun = -1, unfinished = -1;
-  bool before = false;  // the run's item began before the block's range
-  for (int w = 0; w <= kDecWarps; ++w) {
-    const int head = w < kDecWarps ? s_head[w] : -1;
-    const bool ended = head >= 0;
-    if (ended && run < 0) {
-      run = head;
-      from = w;
-      before = true;
-    }
-    if (run >= 0 && (ended || w == kDecWarps)) {
-      float* dst = nullptr;
-      if (!ended || before) {
-        dst = p.part + ((size_t)bid * 2 + (before ? 0 : 1)) * p.part_stride;
-        if (before) begun = run; else unfinished = run;
-      }
-      join_warps<D, NB>(p, run, from, w, ended, s_tail, s_stat, smem,
-                        p.warp_part + (size_t)bid * kDecWarps * p.part_stride, dst);
-      run = -1;
-    }
-    if (w < kDecWarps && s_tail[w] >= 0 && run < 0) {
-      run = s_tail[w];
-      from = w;
-      before = s_mid[w] != 0;
-    }
-  }
-  if (tid == 0) {
-    p.begun[bid] = begun;
-    p.unfinished[bid] = unfinished;
   }
 }
 
 // ---------------------------------------------------------------------------
-// Join of items cut between blocks: block (b, head) takes the item that begins
-// in block b of the main kernel and ends past it, with the partials of the
-// blocks behind it in order.
+// Join of cut items. An item that begins in warp w's range and goes on past it
+// has its partials in slot 1 of w and in slot 0 of the warps behind it. A block
+// has the items that begin in kJoinWarps successive ranges, and one head of
+// them. An item of up to 32 partials is one warp's; longer ones (at most one
+// begins within so few ranges) are the whole block's.
 // ---------------------------------------------------------------------------
-template <int D, int NB>
-__global__ void __launch_bounds__(D) decode_join_kernel(const __grid_constant__ DecodeParams p,
-                                                        int blocks) {
-  using Cfg = DecodeCfg<D, NB>;
-  constexpr int HEADS = Cfg::HEADS;
-  __shared__ int s_n;
-  grid_dependency_wait();
-  const int b0 = blockIdx.x, hl = blockIdx.y, tid = threadIdx.x;
-  const int item = p.unfinished[b0];
-  if (item < 0) return;
-  const int token = item / p.per_token, cc = item % p.per_token;
-  const int hk = cc / p.nsub, sub = cc % p.nsub;
-  if (hl >= min(HEADS, p.G - sub * HEADS)) return;
-  if (tid == 0) s_n = blocks - b0 - 1;
-  __syncthreads();
-  for (int i = tid; b0 + 1 + i < blocks; i += D)
-    if (p.begun[b0 + 1 + i] != item) {
-      atomicMin(&s_n, i);
-      break;
-    }
-  __syncthreads();
-  const int n = s_n;  // further blocks
-  const float* first = p.part + ((size_t)b0 * 2 + 1) * p.part_stride;
-  const float* rest = p.part + (size_t)(b0 + 1) * 2 * p.part_stride;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinPart = 512;  // partials whose weights are held at a time
+
+__device__ __forceinline__ void add_scaled(float4& a, const float4& x, float f) {
+  a.x += x.x * f;
+  a.y += x.y * f;
+  a.z += x.z * f;
+  a.w += x.w * f;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+  return x;
+}
+// Elements 4 col .. 4 col + 3 of a head's result.
+__device__ __forceinline__ void store_joined(const DecodeParams& p, int D, size_t oi, int col, float4 a, float M,
+                                             float MV, float L) {
+  const float f = final_factor(M, MV, L);
+  if (L == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);  // no row: 0, whatever the sums hold
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * f, a.y * f), hi = __floats2bfloat162_rn(a.z * f, a.w * f);
+  *reinterpret_cast<uint2*>(p.out + oi * D + col * 4) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (col == 0 && p.lse != nullptr) p.lse[oi] = final_lse(M, L);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int LANES = D / 4;  // threads of a row
+  __shared__ float s_l[kJoinPart], s_v[kJoinPart];
+  __shared__ float s_red[kJoinWarps][2];
+  __shared__ float4 s_acc[kJoinThreads / LANES][LANES];
+  __shared__ int s_long;        // range in which an item of more than 32 partials begins
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hl = blockIdx.y;
+  const int w0 = blockIdx.x * kJoinWarps;
   const size_t step = (size_t)2 * p.part_stride;
   const int so = p.part_heads * D + hl * 4;
-  const float4 f = *reinterpret_cast<const float4*>(first + so);
-  float M = f.x, MV = f.y;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2 st = *reinterpret_cast<const float2*>(rest + i * step + so);
-    M = fmaxf(M, st.x);
-    MV = fmaxf(MV, st.y);
+  if (tid == 0) s_long = -1;
+  grid_dependency_wait();
+  __syncthreads();
+  if (const int w = w0 + warp; w < p.warps) {
+    const DecodeRange a = p.range[w], b = p.range[w + 1];
+    DecodeRange r{-1, 0, 0, 0};  // ranges w + 1 ..: those that hold a part of the item
+    if (w + 1 + lane < p.warps) r = p.range[w + 1 + lane];
+    const DecodeItem it = item_of(p, max(b.item, 0));
+    // an item begins in range w and goes on past it
+    if (b.tiles > 0 && b.tile > 0 && (a.item != b.item || a.tile == 0) && hl < it.nh) {
+      const uint32_t held = __ballot_sync(0xffffffffu, r.tiles > 0 && r.item == b.item);
+      if (held == 0xffffffffu) {
+        if (lane == 0) s_long = w;
+      } else {
+        const int n = __popc(held) + 1;
+        const float* first = p.part + ((size_t)w * 2 + 1) * p.part_stride;
+        const float* rest = p.part + (size_t)(w + 1) * 2 * p.part_stride - step;  // partial k at rest + k step
+        float4 st = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+        if (lane < n) st = *reinterpret_cast<const float4*>((lane == 0 ? first : rest + lane * step) + so);
+        const float M = warp_max(st.x), MV = warp_max(st.y);
+        const float L = warp_sum(lane < n ? st.z * exp2f(st.x - M) : 0.f);
+        const float f = exp2f(st.y - MV);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int row = lane / LANES, col = lane % LANES;
+#pragma unroll 8
+        for (int k0 = 0; k0 < n; k0 += 32 / LANES) {
+          const int k = k0 + row;
+          const float fk = __shfl_sync(0xffffffffu, f, k);
+          if (k < n)
+            add_scaled(acc, *reinterpret_cast<const float4*>((k == 0 ? first : rest + k * step) + hl * D + col * 4), fk);
+        }
+        if constexpr (LANES == 16) {
+          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+        }
+        if (row == 0) store_joined(p, D, (size_t)it.token * p.H + it.h0 + hl, col, acc, M, MV, L);
+      }
+    }
   }
-  float L = f.z * exp2f(f.x - M);
-  float A = first[hl * D + tid] * exp2f(f.y - MV);
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float4 st = *reinterpret_cast<const float4*>(rest + i * step + so);
-    L += st.z * exp2f(st.x - M);
-    A += rest[i * step + hl * D + tid] * exp2f(st.y - MV);
+  __syncthreads();
+  const int w = s_long;
+  if (w < 0) return;
+  const int item = p.range[w + 1].item;
+  const DecodeItem it = item_of(p, item);
+  const float* first = p.part + ((size_t)w * 2 + 1) * p.part_stride;
+  const float* rest = p.part + (size_t)(w + 1) * 2 * p.part_stride - step;
+  // partials and their maxima
+  int n = 1;
+  float2 top = *reinterpret_cast<const float2*>(first + so);
+  for (int k = 1 + tid;; k += kJoinThreads) {
+    bool mine = w + k < p.warps;
+    if (mine) {
+      const DecodeRange r = p.range[w + k];
+      mine = r.tiles > 0 && r.item == item;
+    }
+    if (mine) {
+      const float2 f = *reinterpret_cast<const float2*>(rest + k * step + so);
+      top.x = fmaxf(top.x, f.x);
+      top.y = fmaxf(top.y, f.y);
+    }
+    const int got = __syncthreads_count(mine);
+    n += got;
+    if (got < kJoinThreads) break;
   }
-  const size_t oi = (size_t)token * p.H + hk * p.G + sub * HEADS + hl;
-  p.out[oi * D + tid] = __float2bfloat16(L == 0.f ? 0.f : A * final_factor(M, MV, L));
-  if (tid == 0 && p.lse != nullptr) p.lse[oi] = final_lse(M, L);
+  float M = warp_max(top.x), MV = warp_max(top.y);
+  if (lane == 0) s_red[warp][0] = M, s_red[warp][1] = MV;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kJoinWarps; ++k) {
+    M = fmaxf(M, s_red[k][0]);
+    MV = fmaxf(MV, s_red[k][1]);
+  }
+  // sums, in the partials' order
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int row = tid / LANES, col = tid % LANES;
+  for (int base = 0; base < n; base += kJoinPart) {
+    const int cnt = min(kJoinPart, n - base);
+    for (int i = tid; i < cnt; i += kJoinThreads) {
+      const int k = base + i;
+      const float4 f = *reinterpret_cast<const float4*>((k == 0 ? first : rest + k * step) + so);
+      s_l[i] = f.z * exp2f(f.x - M);
+      s_v[i] = exp2f(f.y - MV);
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int i = row; i < cnt; i += kJoinThreads / LANES) {
+      const int k = base + i;
+      add_scaled(acc, *reinterpret_cast<const float4*>((k == 0 ? first : rest + k * step) + hl * D + col * 4), s_v[i]);
+    }
+    if (warp == 0)
+      for (int i = lane; i < cnt; i += 32) L += s_l[i];
+    __syncthreads();
+  }
+  s_acc[row][col] = acc;
+  L = warp_sum(L);
+  __syncthreads();
+  if (tid < LANES) {  // these are warp 0's threads
+    float4 a = s_acc[0][tid];
+#pragma unroll
+    for (int k = 1; k < kJoinThreads / LANES; ++k) add_scaled(a, s_acc[k][tid], 1.f);
+    store_joined(p, D, (size_t)it.token * p.H + it.h0 + hl, tid, a, M, MV, L);
+  }
 }
 
 }  // namespace dil

@@ -1256,27 +1256,30 @@ extern "C" int dilattn_cache_read(const void* kc, const void* vc, const float* k
 namespace dil {
 namespace {
 
-// Workspace of a decode: tile counts, their sums, and the partials of items cut
-// between blocks or warps.
-struct DecodeScratch {
-  size_t counts, sums, marks, part, warp_part;
-  size_t total() const { return counts + sums + marks + part + warp_part; }
-};
-int decode_blocks(int G) { return kDecMaxBlocks / (G <= 8 ? 1 : 2); }
-int decode_part_heads(int G) { return std::min(G, G <= 8 ? 8 : 16); }
+// Heads of an item, a power of two up to 8, or 16: what a decode kernel is made for.
+int decode_heads(int G) { return G <= 2 ? G : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
 long long decode_items(int T, int Hkv, int G) {
-  const int heads = G <= 8 ? 8 : 16;
+  const int heads = decode_heads(G);
   return (long long)T * Hkv * ((G + heads - 1) / heads);
 }
+int decode_blocks_per_sm(int G, int d) { return (d == 64 ? 4 : 3) - (G > 8 ? 1 : 0); }
+
+// Workspace of a decode: the items' walks, the warps' ranges, and the partials of cut items.
+struct DecodeScratch {
+  size_t head, walk, upto, sums, range, part;
+  size_t total() const { return head + walk + upto + sums + range + part; }
+};
 DecodeScratch decode_scratch(int T, int H, int Hkv, int d) {
   const int G = H / Hkv;
-  const size_t blocks = decode_blocks(G), part = (size_t)decode_part_heads(G) * (d + 4) * 4;
+  const size_t items = (size_t)decode_items(T, Hkv, G);
+  const size_t warps = (size_t)kDecMaxSms * decode_blocks_per_sm(G, d) * kDecWarps;
   DecodeScratch s;
-  s.counts = align256((size_t)decode_items(T, Hkv, G) * 4);
-  s.sums = align256(kDecGroups * 8);
-  s.marks = align256(blocks * 2 * 4);
-  s.part = align256(blocks * 2 * part);
-  s.warp_part = align256(blocks * kDecWarps * part);
+  s.head = align256(items * sizeof(DecodeHead));
+  s.walk = align256(items * kMaxPat * sizeof(DecodeWalk));
+  s.upto = align256(items * 8);
+  s.sums = align256(kPlanThreads * 8);
+  s.range = align256((warps + 1) * sizeof(DecodeRange));
+  s.part = align256(warps * 2 * std::min(G, decode_heads(G)) * (d + 4) * 4);
   return s;
 }
 
@@ -1300,22 +1303,35 @@ cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int NB, int FMT>
-cudaError_t launch_decode(const DecodeParams& p, int blocks, cudaStream_t stream) {
-  using Cfg = DecodeCfg<D, NB>;
-  const int groups = (p.items + p.group - 1) / p.group;
-  decode_plan_kernel<Cfg::TR, Cfg::HEADS><<<groups, kDecWarps * 32, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+template <int D, int HEADS, int FMT>
+cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
+  const int groups = (int)(((long long)p.items + p.group - 1) / p.group);
+  cudaError_t e;
+  if (p.group == 1) {
+    decode_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, 1);
+    e = cudaGetLastError();
+  } else {
+    decode_walks_kernel<<<groups, kWalkThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess)
+      e = launch_overlapped(decode_plan_kernel, dim3(1), kPlanThreads, 0, stream, p, 0);
+  }
   if (e != cudaSuccess) return e;
-  // opting into this much shared memory is needed once per device; it costs nothing to repeat
-  e = cudaFuncSetAttribute(decode_kernel<D, NB, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Cfg::SMEM_BYTES);
+  e = launch_overlapped(decode_kernel<D, HEADS, FMT>, dim3((unsigned)(p.warps / kDecWarps)),
+                        kDecWarps * 32, 0, stream, p);
   if (e != cudaSuccess) return e;
-  e = launch_overlapped(decode_kernel<D, NB, FMT>, dim3((unsigned)blocks), kDecWarps * 32,
-                        Cfg::SMEM_BYTES, stream, p);
-  if (e != cudaSuccess || blocks == 1) return e;
-  return launch_overlapped(decode_join_kernel<D, NB>, dim3((unsigned)blocks, (unsigned)p.part_heads),
-                           D, 0, stream, p, blocks);
+  const dim3 grid((unsigned)((p.warps + kJoinWarps - 1) / kJoinWarps), (unsigned)p.part_heads);
+  return launch_overlapped(decode_join_kernel<D>, grid, kJoinThreads, 0, stream, p);
+}
+template <int D, int FMT>
+cudaError_t launch_decode_heads(const DecodeParams& p, cudaStream_t stream) {
+  switch (p.heads) {
+    case 1: return launch_decode<D, 1, FMT>(p, stream);
+    case 2: return launch_decode<D, 2, FMT>(p, stream);
+    case 4: return launch_decode<D, 4, FMT>(p, stream);
+    case 8: return launch_decode<D, 8, FMT>(p, stream);
+    default: return launch_decode<D, 16, FMT>(p, stream);
+  }
 }
 
 // Inverse of an odd number modulo 2^32: Newton's step doubles the correct low bits.
@@ -1331,6 +1347,7 @@ void decode_patterns(DecodeParams& p, const int* w, const int* r, int npat) {
   for (int i = 0; i < npat; ++i) order[i] = i;
   std::stable_sort(order, order + npat, [&](int a, int b) { return r[a] < r[b]; });
   p.npat = npat;
+  p.dense = npat == 1 && r[0] == 1;
   for (int i = 0; i < npat; ++i) {
     p.w[i] = w[order[i]];
     p.r[i] = r[order[i]];
@@ -1414,47 +1431,42 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   p.qk_scale = (float)(1.4426950408889634 / std::sqrt((double)d));
   decode_patterns(p, w, r, npat);
   p.G = H / Hkv;
-  const int nb = p.G <= 8 ? 1 : 2;
-  p.nsub = (p.G + 8 * nb - 1) / (8 * nb);
+  p.heads = decode_heads(p.G);
+  p.nsub = (p.G + p.heads - 1) / p.heads;
   p.per_token = Hkv * p.nsub;
   divisor_magic((uint32_t)p.per_token, p.pt_mul, p.pt_sh);
   divisor_magic((uint32_t)p.nsub, p.ns_mul, p.ns_sh);
   p.items = (int)decode_items(T, Hkv, p.G);
-  // a plan block sums a group of items, eight (one a warp) while the sums' array lasts
-  p.group = kDecWarps * ((p.items + kDecWarps * kDecGroups - 1) / (kDecWarps * kDecGroups));
+  // up to kPlanThreads groups, which one block sums; one item each while they last
+  p.group = p.items <= kPlanThreads
+                ? 1
+                : kWalkThreads * (int)((p.items + (long long)kWalkThreads * kPlanThreads - 1) /
+                                       ((long long)kWalkThreads * kPlanThreads));
   const DecodeScratch lay = decode_scratch(T, H, Hkv, d);
-  char* wsb = reinterpret_cast<char*>(workspace);
-  p.counts = reinterpret_cast<int*>(wsb);
-  p.sums = reinterpret_cast<long long*>(wsb + lay.counts);
-  p.begun = reinterpret_cast<int*>(wsb + lay.counts + lay.sums);
-  p.unfinished = p.begun + decode_blocks(p.G);
-  p.part = reinterpret_cast<float*>(wsb + lay.counts + lay.sums + lay.marks);
-  p.warp_part = reinterpret_cast<float*>(wsb + lay.counts + lay.sums + lay.marks + lay.part);
-  p.part_heads = decode_part_heads(p.G);
+  char* at = reinterpret_cast<char*>(workspace);
+  auto take = [&at](size_t n) { return at += n, at - n; };
+  p.head = reinterpret_cast<DecodeHead*>(take(lay.head));
+  p.walk = reinterpret_cast<DecodeWalk*>(take(lay.walk));
+  p.upto = reinterpret_cast<long long*>(take(lay.upto));
+  p.sums = reinterpret_cast<long long*>(take(lay.sums));
+  p.range = reinterpret_cast<DecodeRange*>(take(lay.range));
+  p.part = reinterpret_cast<float*>(take(lay.part));
+  p.part_heads = std::min(p.G, p.heads);
   p.part_stride = p.part_heads * (d + 4);
-  // the most rows that an item can have: no more blocks than give each warp two tiles
+  // the most tiles that there can be: no more warps than have work
   const long long longest = (long long)max_pages * page_size;
   double rows = 0;
   for (int i = 0; i < npat; ++i) rows += (double)std::min<long long>(w[i], longest) / r[i] + 1;
-  const double tiles = (rows / (d == 128 ? 16 : 32) + npat) * p.items;
-  int blocks = std::min(st->num_sms * (nb == 1 ? 2 : 1), decode_blocks(p.G));
-  blocks = (int)std::min<double>(blocks, tiles / (2 * kDecWarps) + 1);
+  const double tiles = (rows / kDecTile + npat) * p.items;
+  p.least = 2;
+  const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(p.G, d);
+  p.warps = kDecWarps * (int)std::min<double>(blocks, tiles / (kDecWarps * p.least) + 1);
+  if (tiles / p.warps > 2147483647.0) return DILATTN_ERR_UNSUPPORTED;  // a range's tiles are an int
   cudaError_t e;
-  if (format == DILATTN_CACHE_E4M3) {
-    if (nb == 1)
-      e = d == 64 ? launch_decode<64, 1, kFmtE4M3>(p, blocks, stream)
-                  : launch_decode<128, 1, kFmtE4M3>(p, blocks, stream);
-    else
-      e = d == 64 ? launch_decode<64, 2, kFmtE4M3>(p, blocks, stream)
-                  : launch_decode<128, 2, kFmtE4M3>(p, blocks, stream);
-  } else {
-    if (nb == 1)
-      e = d == 64 ? launch_decode<64, 1, kFmtInt8>(p, blocks, stream)
-                  : launch_decode<128, 1, kFmtInt8>(p, blocks, stream);
-    else
-      e = d == 64 ? launch_decode<64, 2, kFmtInt8>(p, blocks, stream)
-                  : launch_decode<128, 2, kFmtInt8>(p, blocks, stream);
-  }
+  if (format == DILATTN_CACHE_E4M3)
+    e = d == 64 ? launch_decode_heads<64, kFmtE4M3>(p, stream) : launch_decode_heads<128, kFmtE4M3>(p, stream);
+  else
+    e = d == 64 ? launch_decode_heads<64, kFmtInt8>(p, stream) : launch_decode_heads<128, kFmtInt8>(p, stream);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   return DILATTN_OK;
 }

@@ -1,4 +1,4 @@
-"""Build libdilattn.so in-tree with nvcc for sm_100a.
+"""Build libdilattn.so (nvcc, sm_100a) and the binding's _torch_calls.so (g++) in-tree.
 
     python -m sparse_long_sequence_dilated_b200.build [--ptxas-v]
 """
@@ -14,6 +14,8 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "dilattn.cu")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdilattn.so")
+CALLS_SRC = os.path.join(PKG, "csrc", "torch_calls.cpp")
+CALLS = os.path.join(PKG, "_torch_calls.so")
 
 
 def nvcc_path() -> str:
@@ -41,6 +43,31 @@ def build(ptxas_verbose: bool = False, out: str = LIB) -> str:
     return out
 
 
+def build_calls(out: str = CALLS) -> str:
+    """The binding's compiled calls, against this interpreter's torch (whose libraries are
+    loaded before it)."""
+    import sysconfig
+
+    import torch
+
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    cmd = [
+        shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I", INCLUDE, "-I", os.path.join(top, "include"),
+        "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+        "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+        "-o", out, CALLS_SRC, "-L", os.path.join(top, "lib"),
+        "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+    ]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    return out
+
+
 if __name__ == "__main__":
     build(ptxas_verbose="--ptxas-v" in sys.argv)
+    build_calls()
     print(LIB)

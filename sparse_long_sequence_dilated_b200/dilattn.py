@@ -1,12 +1,14 @@
-"""Thin ctypes binding of libdilattn (include/dilattn.h).
+"""Thin binding of libdilattn (include/dilattn.h).
 
 The ``dilattn_*`` functions mirror the C entry points one to one (integer
 device pointers and sizes). The torch-facing functions (``fwd``,
 ``fwd_train``, ``bwd``, ``fwd_fp8``, ``fwd_noalloc``, ``fwd_seqpar``,
-``pack_dilated``, ``selection``, ``cache_write``, ``cache_read``, ``decode``) add only argument marshalling for torch
-tensors: checks of every tensor's shape, dtype, layout and device (the C
-entry points take bare pointers and cannot see a buffer's size), output and
-workspace allocation with torch, and the current CUDA stream. Every step of the
+``pack_dilated``, ``selection``, ``cache_write``, ``cache_read``, ``decode``)
+add only argument marshalling for torch tensors: checks of every tensor's
+shape, dtype, layout and device (the C entry points take bare pointers and
+cannot see a buffer's size), output and workspace allocation with torch, and
+the current CUDA stream. The last three, whose kernels take microseconds, do
+that in C++ (csrc/torch_calls.cpp) for their plain form. Every step of the
 computation runs in the library's CUDA kernels; there is no other code path,
 and a missing or unloadable library raises.
 """
@@ -19,6 +21,7 @@ from typing import Any, NamedTuple, Optional, Sequence, Tuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libdilattn.so")
+CALLS_PATH = os.path.join(PKG, "_torch_calls.so")
 
 DILATTN_OK = 0
 MAX_PATTERNS = 16
@@ -401,6 +404,25 @@ def fwd_fp8(q8, k8, v, patterns, q_scale: float, k_scale: float, causal: bool = 
 # ---------------------------------------------------------------------------
 # the 8-bit key/value cache and the attention over it
 # ---------------------------------------------------------------------------
+_calls_module = None
+
+
+def _calls():
+    """The compiled marshalling of the cache calls (csrc/torch_calls.cpp). Each of its functions
+    makes the plain form of a call, or returns None without having done anything."""
+    global _calls_module
+    if _calls_module is None:
+        for path in (LIB_PATH, CALLS_PATH):
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: build it with "
+                                   "`python -m sparse_long_sequence_dilated_b200.build`")
+        _torch()  # its libraries first
+        from . import _torch_calls
+        _torch_calls.bind(LIB_PATH)
+        _calls_module = _torch_calls
+    return _calls_module
+
+
 class Cache(NamedTuple):
     """A paged 8-bit key/value cache: the four device arrays dilattn_cache_write fills.
 
@@ -490,6 +512,10 @@ def cache_write(cache: Cache, k, v, table, start, offsets=None, stream=None) -> 
     into the pages that table [B, max_pages] int32 names. Sequence b's rows are
     offsets[b]:offsets[b + 1] (int32 [B + 1]; None: one row for each sequence) and go to positions
     start[b], start[b] + 1, ... (int32 [B])."""
+    if stream is None:
+        done = (_calls_module or _calls()).cache_write(*cache, table, k, v, start, offsets)
+        if done is not None:
+            return _check(done[0], "dilattn_cache_write")
     dev, c, (tp, B, mp) = _cache_args(cache, table)
     Hkv, d = c[5], c[7]
     T = int(k.shape[0]) if k.dim() == 3 else -1
@@ -507,6 +533,11 @@ def cache_read(cache: Cache, table, start, offsets=None, total: Optional[int] = 
                v=None, stream=None):
     """dilattn_cache_read: (k, v), bf16 [total, Hkv, d], of the tokens that offsets and start name
     (as in cache_write). Rows at and past offsets[B] are left as they were."""
+    if stream is None and k is None and v is None:
+        done = (_calls_module or _calls()).cache_read(*cache, table, start, offsets, total)
+        if done is not None:
+            _check(done[0], "dilattn_cache_read")
+            return done[1], done[2]
     torch = _torch()
     dev, c, (tp, B, mp) = _cache_args(cache, table)
     Hkv, d = c[5], c[7]
@@ -546,6 +577,12 @@ def decode(q, cache: Cache, table, pos, patterns, seq=None, out=None, lse=None, 
     to sequence i) over the cached positions up to and including their own.
 
     Returns (out [T, H, d] bf16, lse [T, H] float32)."""
+    if stream is None:
+        done = (_calls_module or _calls()).decode(*cache, table, q, pos, patterns, seq, out, lse,
+                                                  workspace)
+        if done is not None:
+            _check(done[0], "dilattn_decode")
+            return done[1], done[2]
     torch = _torch()
     dev, c, (tp, B, mp) = _cache_args(cache, table)
     Hkv, d = c[5], c[7]

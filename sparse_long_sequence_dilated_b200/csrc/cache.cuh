@@ -10,6 +10,13 @@
 
 namespace dil {
 
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 enum CacheFmt : int { kFmtE4M3 = 0, kFmtInt8 = 1 };
 
 // The part of a cache's addressing that every kernel needs.
@@ -107,90 +114,181 @@ struct CacheWriteParams {
   float* scale[2];
 };
 
-// One block per (touched page, KV head, K or V): the page's new rows, its
-// scale and, when that grows, the codes already there. A sequence of n tokens
-// touches at most floor(n / P) + 2 pages, so sequence b owns the page slots
-// from floor(offset_b / P) + 2 b up to the next sequence's first.
+// Largest magnitude of eight bf16 numbers, as their bits compare: infinities and NaN are 0x7f80 and above.
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, const uint4& u) {
+  m = max(max(m, u.x & 0x7fffu), (u.x >> 16) & 0x7fffu);
+  m = max(max(m, u.y & 0x7fffu), (u.y >> 16) & 0x7fffu);
+  m = max(max(m, u.z & 0x7fffu), (u.z >> 16) & 0x7fffu);
+  return max(max(m, u.w & 0x7fffu), (u.w >> 16) & 0x7fffu);
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t encode_bf16x4(uint32_t a, uint32_t b, float inv) {
+  return encode4<FMT>(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
+                      __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv);
+}
+
+// The scale of a page and head after rows of this largest magnitude come to one
+// that held `was` (0: the page starts afresh); NaN for numbers that no code holds.
+template <int FMT>
+__device__ __forceinline__ float next_scale(uint32_t amax, float was) {
+  return amax >= 0x7f80u || was != was ? __uint_as_float(0x7fffffffu) : fmaxf(block_scale<FMT>(amax << 16), was);
+}
+
+// Rounds a page and head's codes again, rows r0 .. r1 - 1 aside, by `threads` threads from `tid` on.
 template <int D, int FMT>
-__global__ void __launch_bounds__(128) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
-  __shared__ int s_seq;
-  __shared__ uint32_t s_amax[4];
-  const int tid = threadIdx.x, h = blockIdx.y, z = blockIdx.z;
-  const int P = 1 << p.geom.lp;
-  if (tid == 0) s_seq = -1;
-  __syncthreads();
-  for (int b = tid; b < p.geom.B; b += 128) {
-    int lo, n;
-    token_range(p.tok, b, lo, n);
-    const long long first = (lo >> p.geom.lp) + 2ll * b;
-    const long long last = ((lo + n) >> p.geom.lp) + 2ll * b + 2;
-    if (first <= (long long)blockIdx.x && (long long)blockIdx.x < last) s_seq = b;
+__device__ __forceinline__ void rescale_rows(uint8_t* codes, int P, int r0, int r1, float ratio, int tid, int threads) {
+  for (int i = tid; i < P * (D / 16); i += threads) {
+    const int row = i / (D / 16);
+    if (row >= r0 && row < r1) continue;
+    uint4* at = reinterpret_cast<uint4*>(codes) + i;
+    const uint4 u = *at;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[4];
+      decode4<FMT>(w[k], f);
+      o[k] = encode4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+    }
+    *at = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  __syncthreads();
-  const int b = s_seq;
-  if (b < 0) return;
-  int off, n;
-  token_range(p.tok, b, off, n);
-  const int start = p.tok.start[b];
-  if (n == 0) return;
-  if (start < 0 || start > 0x7fffffff - n) {
+}
+
+// One token of each sequence: a warp for each (sequence, KV head, K or V).
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant__ CacheWriteParams p) {
+  constexpr int C = D / 64;  // 32-bit words of two numbers that a lane has
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int h = (int)(unit % p.geom.Hkv);
+  const int z = (int)(unit / p.geom.Hkv) & 1, b = (int)(unit / p.geom.Hkv >> 1);
+  grid_dependency_wait();
+  if (b >= p.geom.B) return;
+  const int pos = p.tok.start[b];
+  if (pos < 0) {
     p.geom.err.raise(kErrBadPage);
     return;
   }
-  const int pg = (start >> p.geom.lp) + (int)((long long)blockIdx.x - (off >> p.geom.lp) - 2ll * b);
-  const long long row0 = (long long)pg << p.geom.lp;
-  const int lo = (int)max((long long)start, row0), hi = (int)min((long long)start + n, row0 + P);
-  if (lo >= hi) return;
-  const int page = page_of(p.geom, b, lo);
+  uint32_t x[C];
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(p.x[z] + (long long)b * p.stride[z] + (long long)h * D);
+  if constexpr (C == 2) {
+    const uint2 u = reinterpret_cast<const uint2*>(src)[lane];
+    x[0] = u.x, x[1] = u.y;
+  } else {
+    x[0] = src[lane];
+  }
+  const int page = page_of(p.geom, b, pos);
   if (page < 0) return;
-
-  const __nv_bfloat16* x = p.x[z] + (long long)(off + lo - start) * p.stride[z] + (long long)h * D;
+  const int row = pos & ((1 << p.geom.lp) - 1);
   uint8_t* codes = p.codes[z] + (((size_t)page * p.geom.Hkv + h) << p.geom.lp) * D;
   float* scale = p.scale[z] + (size_t)page * p.geom.Hkv + h;
-  constexpr int V = D / 8;  // 16-byte pieces of a row
-  const int pieces = (hi - lo) * V;
-  // bf16 magnitudes compare as integers; infinities and NaN are 0x7f80 and above
+  const float was = row == 0 ? 0.f : *scale;
   uint32_t amax = 0;
-  for (int i = tid; i < pieces; i += 128) {
-    const uint4 u = *reinterpret_cast<const uint4*>(x + (long long)(i / V) * p.stride[z] + (i % V) * 8);
-    amax = max(max(amax, u.x & 0x7fffu), (u.x >> 16) & 0x7fffu);
-    amax = max(max(amax, u.y & 0x7fffu), (u.y >> 16) & 0x7fffu);
-    amax = max(max(amax, u.z & 0x7fffu), (u.z >> 16) & 0x7fffu);
-    amax = max(max(amax, u.w & 0x7fffu), (u.w >> 16) & 0x7fffu);
-  }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  if ((tid & 31) == 0) s_amax[tid >> 5] = amax;
-  const bool fresh = lo == row0;
-  const float was = fresh ? 0.f : *scale;
-  __syncthreads();
-  amax = max(max(s_amax[0], s_amax[1]), max(s_amax[2], s_amax[3]));
-  const bool poisoned = amax >= 0x7f80u || was != was;
-  float now = poisoned ? __uint_as_float(0x7fffffffu) : fmaxf(block_scale<FMT>(amax << 16), was);
-  const float inv = poisoned ? 0.f : 1.f / now;
-  if (!fresh && now > was) {
-    const float ratio = was * inv;
-    for (int i = tid; i < P * (D / 4); i += 128) {
-      const int row = i / (D / 4);
-      if (row >= lo - row0 && row < hi - row0) continue;
-      uint32_t* w = reinterpret_cast<uint32_t*>(codes) + i;
-      float f[4];
-      decode4<FMT>(*w, f);
-      *w = encode4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
-    }
-  }
-  for (int i = tid; i < pieces; i += 128) {
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (!poisoned)
-      u = *reinterpret_cast<const uint4*>(x + (long long)(i / V) * p.stride[z] + (i % V) * 8);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float f[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16) * inv;
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * inv;
+  for (int i = 0; i < C; ++i) amax = max(max(amax, x[i] & 0x7fffu), (x[i] >> 16) & 0x7fffu);
+  const float now = next_scale<FMT>(__reduce_max_sync(0xffffffffu, amax), was);
+  const bool poisoned = now != now;
+  const float inv = poisoned ? 0.f : 1.f / now;
+  if (row != 0 && now > was) rescale_rows<D, FMT>(codes, 1 << p.geom.lp, row, row + 1, was * inv, lane, 32);
+  if (poisoned)
+#pragma unroll
+    for (int i = 0; i < C; ++i) x[i] = 0;
+  if constexpr (C == 2) {
+    reinterpret_cast<uint32_t*>(codes + (size_t)row * D)[lane] = encode_bf16x4<FMT>(x[0], x[1], inv);
+  } else {
+    reinterpret_cast<uint16_t*>(codes + (size_t)row * D)[lane] = (uint16_t)encode_bf16x4<FMT>(x[0], 0u, inv);
+  }
+  if (lane == 0) *scale = now;
+}
+
+// First page slot of sequence b. A sequence of n tokens touches at most
+// floor(n / P) + 2 pages, so it owns the slots up to the next sequence's first.
+__device__ __forceinline__ long long first_slot_of(const CacheWriteParams& p, int b) {
+  int lo, n;
+  token_range(p.tok, b, lo, n);
+  return (lo >> p.geom.lp) + 2ll * b;
+}
+
+// Ragged stretches: W warps for each (touched page, KV head, K or V), with all
+// of its new rows in registers, 64 numbers a lane, so that they are read once.
+// Heads are the fastest index: blocks that run together read whole rows.
+template <int D, int FMT, int W>
+__global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
+  constexpr int V = D / 16;  // pieces of 16 numbers of a row
+  __shared__ uint32_t s_amax[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x % (W * 32);  // in the unit
+  const long long unit = (long long)blockIdx.x * (8 / W) + warp / W;
+  const int h = (int)(unit % p.geom.Hkv);
+  const int z = (int)(unit / p.geom.Hkv) & 1;
+  const long long slot = unit / p.geom.Hkv >> 1;
+  const int P = 1 << p.geom.lp;
+  grid_dependency_wait();
+  // the slot's sequence: the last one whose first slot is at or before it
+  int b = 0;
+  for (int span = p.geom.B; span > 1;) {
+    const int step = (span + 31) / 32, at = b + lane * step;
+    const bool in = lane * step < span && first_slot_of(p, at) <= slot;
+    const int k = max(__popc(__ballot_sync(0xffffffffu, in)) - 1, 0);
+    b += k * step;
+    span = min(step, span - k * step);
+  }
+  int off, n;
+  token_range(p.tok, b, off, n);
+  const int start = p.tok.start[b];
+  int lo = 0, hi = 0, page = -1;
+  long long row0 = 0;
+  if (n > 0) {
+    if (start < 0 || start > 0x7fffffff - n) {
+      if (tid == 0) p.geom.err.raise(kErrBadPage);
+    } else {
+      row0 = ((long long)(start >> p.geom.lp) + slot - first_slot_of(p, b)) << p.geom.lp;
+      lo = (int)min(max((long long)start, row0), 0x7fffffffll);
+      hi = (int)min((long long)start + n, row0 + P);
+      if (lo < hi) page = page_of(p.geom, b, lo);
     }
-    *reinterpret_cast<uint2*>(codes + (size_t)(lo - row0 + i / V) * D + (i % V) * 8) =
-        make_uint2(encode4<FMT>(f[0], f[1], f[2], f[3]), encode4<FMT>(f[4], f[5], f[6], f[7]));
+  }
+  const bool work = page >= 0;
+  const __nv_bfloat16* x = p.x[z] + (long long)(off + lo - start) * p.stride[z] + (long long)h * D;
+  const int r0 = (int)(lo - row0), rows = work ? hi - lo : 0;
+  const size_t blk = work ? (size_t)page * p.geom.Hkv + h : 0;
+  uint8_t* codes = p.codes[z] + (blk << p.geom.lp) * D;
+  float* scale = p.scale[z] + blk;
+  uint4 u[4][2];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = tid + i * W * 32;
+    u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
+    if (k / V < rows) {
+      const uint4* src = reinterpret_cast<const uint4*>(x + (long long)(k / V) * p.stride[z] + (k % V) * 16);
+      u[i][0] = src[0], u[i][1] = src[1];
+    }
+  }
+  const float was = work && r0 > 0 ? *scale : 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) amax = max_magnitude(max_magnitude(amax, u[i][0]), u[i][1]);
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if constexpr (W > 1) {
+    if (lane == 0) s_amax[warp] = amax;
+    __syncthreads();
+    const int first = warp / W * W;
+#pragma unroll
+    for (int i = 0; i < W; ++i) amax = max(amax, s_amax[first + i]);
+  }
+  if (!work) return;
+  const float now = next_scale<FMT>(amax, was);
+  const bool poisoned = now != now;
+  const float inv = poisoned ? 0.f : 1.f / now;
+  if (r0 > 0 && now > was) rescale_rows<D, FMT>(codes, P, r0, r0 + rows, was * inv, tid, W * 32);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = tid + i * W * 32;
+    if (k / V >= rows) continue;
+    if (poisoned) u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(codes + (size_t)r0 * D + (size_t)k * 16) =
+        make_uint4(encode_bf16x4<FMT>(u[i][0].x, u[i][0].y, inv), encode_bf16x4<FMT>(u[i][0].z, u[i][0].w, inv),
+                   encode_bf16x4<FMT>(u[i][1].x, u[i][1].y, inv), encode_bf16x4<FMT>(u[i][1].z, u[i][1].w, inv));
   }
   if (tid == 0) *scale = now;
 }
@@ -211,6 +309,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
   const long long per = (long long)p.geom.Hkv * V;
   const long long total = per * p.tok.T;
   const int z = blockIdx.z;
+  grid_dependency_wait();
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (long long)gridDim.x * 256) {
     const int tok = (int)(i / per), rest = (int)(i % per);

@@ -21,10 +21,14 @@
 // item that is cut leaves partials that decode_join_kernel combines in warp
 // order (no atomics: the same call gives the same bits).
 //
-// Launches: decode_plan_kernel describes every item's walks once and cuts the
-// sequence (in one block up to kPlanThreads items; above, decode_walks_kernel
-// describes them in many), decode_kernel, decode_join_kernel.
+// Launches: decode_plan_kernel, one cluster, describes every item's walks once
+// and cuts the sequence (above kPlanBlocks * kPlanThreads items,
+// decode_walks_kernel describes them before it, over the whole GPU), then
+// decode_kernel, then decode_join_kernel. Each is launched while the one before
+// it runs and waits for that one's end.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "cache.cuh"
 
@@ -33,7 +37,8 @@ namespace dil {
 constexpr int kDecWarps = 4;         // warps of a block
 constexpr int kDecMaxSms = 160;      // the workspace has partials for the warps of this many SMs
 constexpr int kDecTile = 32;         // rows of a tile
-constexpr int kPlanThreads = 1024;   // items that one plan block describes; most groups of items
+constexpr int kPlanBlocks = 8;       // blocks of the plan's cluster
+constexpr int kPlanThreads = 512;    // most groups of items that one of them has
 constexpr int kWalkThreads = 256;
 
 // A warp's range of the tile sequence: its first tile is tile `tile` of item `item`.
@@ -67,7 +72,8 @@ struct DecodeParams {
   uint32_t pt_mul, ns_mul;   // reciprocals of per_token and nsub (divisor_magic)
   int pt_sh, ns_sh;
   int items;
-  int group;                 // items of a group, whose tiles one block sums
+  int group;                 // items of a group: 1, or what a block of decode_walks_kernel describes
+  int lanes;                 // threads that describe an item: a power of two, at least npat
   int warps;                 // warps of the grid
   int least;                 // fewest tiles of a range
   float qk_scale;            // log2(e) / sqrt(d)
@@ -160,70 +166,64 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void grid_dependency_release() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // ---------------------------------------------------------------------------
 // Plan
 // ---------------------------------------------------------------------------
 
-// Writes an item's head and walks; returns its number of tiles. One thread.
+// Writes an item's head and walks; returns its number of tiles. p.lanes threads
+// of a warp work on an item, lane j of them on pattern j; all 32 take part.
 __device__ int describe_item(const DecodeParams& p, int item) {
-  const DecodeItem it = item_of(p, item);
+  const bool real = item < p.items;
+  const DecodeItem it = item_of(p, real ? item : 0);
+  const int j = threadIdx.x & (p.lanes - 1), jj = min(j, p.npat - 1);
   DecodeHead hd;
   hd.b = p.seq != nullptr ? p.seq[it.token] : it.token;
   hd.pos = p.pos[it.token];
   hd.pad = 0;
+  const int r = p.r[jj], w = p.w[jj], r_sh = p.r_sh[jj];
+  const uint32_t r_mul = p.r_mul[jj], w_mul = p.w_mul[jj], div = p.divisors[jj];
+  const int w_sh = p.w_sh[jj];
+  const int skip = it.h0 - (int)udiv((uint32_t)it.h0, r_mul, r_sh) * r;  // h0 mod r
   if (hd.pos >= 0 &&
       ((unsigned)hd.b >= (unsigned)p.geom.B || (hd.pos >> p.geom.lp) >= p.geom.max_pages)) {
-    p.geom.err.raise(kErrBadPage);
+    if (real) p.geom.err.raise(kErrBadPage);
     hd.pos = -1;
   }
   if (hd.pos < 0) hd.b = 0;
-  int start[kMaxPat], tiles = 0;
-  uint32_t in[kMaxPat];
-  for (int j = 0; j < p.npat; ++j) {
-    DecodeWalk wk{0x7fffffff, 0, 0, 0u};
-    if (hd.pos >= 0) {
-      const int r = p.r[j];
-      const int s = (int)udiv((uint32_t)hd.pos, p.w_mul[j], p.w_sh[j]) * p.w[j];
-      const int rel = hd.pos - s;
-      const int steps = (int)udiv((uint32_t)rel, p.r_mul[j], p.r_sh[j]);
-      const int off = rel - steps * r;
-      if (r == 1) {
-        wk.heads = (1u << it.nh) - 1;
-      } else {
-        const int first = off - (it.h0 - (int)udiv((uint32_t)it.h0, p.r_mul[j], p.r_sh[j]) * r);
-        for (uint32_t k = first < 0 ? first + r : first; k < (uint32_t)it.nh; k += (uint32_t)r)
-          wk.heads |= 1u << k;  // k + r stays below 2^32
-      }
-      if (wk.heads != 0) {
-        int limit = 0x7fffffff;
-        for (uint32_t d = p.divisors[j]; d != 0; d &= d - 1) {
-          const int l = __ffs(d) - 1;
-          if ((wk.heads & ~in[l]) == 0) limit = min(limit, start[l]);
-        }
-        wk.s = s;
-        wk.base = s + off;
-        wk.n = steps + 1;
-        if (limit <= hd.pos)
-          wk.n = limit > wk.base
-                     ? (int)udiv((uint32_t)(limit - 1 - wk.base), p.r_mul[j], p.r_sh[j]) + 1
-                     : 0;
-      }
-      start[j] = s;
+  DecodeWalk wk{0x7fffffff, 0, 0, 0u};
+  int s = 0;
+  if (hd.pos >= 0 && j < p.npat) {
+    s = (int)udiv((uint32_t)hd.pos, w_mul, w_sh) * w;
+    const int rel = hd.pos - s;
+    const int steps = (int)udiv((uint32_t)rel, r_mul, r_sh);
+    const int off = rel - steps * r;
+    if (r == 1) {
+      wk.heads = (1u << it.nh) - 1;
+    } else {
+      for (uint32_t k = off < skip ? off - skip + r : off - skip; k < (uint32_t)it.nh; k += (uint32_t)r)
+        wk.heads |= 1u << k;  // k + r stays below 2^32
     }
-    in[j] = wk.heads;
-    tiles += (int)(((uint32_t)wk.n + kDecTile - 1) / kDecTile);
-    p.walk[(size_t)item * p.npat + j] = wk;
+    if (wk.heads != 0) {
+      wk.s = s;
+      wk.base = s + off;
+      wk.n = steps + 1;
+    }
   }
+  int limit = 0x7fffffff;
+  for (int l = 0; l + 1 < p.npat; ++l) {
+    const int sl = __shfl_sync(0xffffffffu, s, l, p.lanes);
+    const uint32_t hl = __shfl_sync(0xffffffffu, wk.heads, l, p.lanes);
+    if ((div >> l & 1u) && (wk.heads & ~hl) == 0) limit = min(limit, sl);
+  }
+  if (wk.n > 0 && limit <= hd.pos)
+    wk.n = limit > wk.base ? (int)udiv((uint32_t)(limit - 1 - wk.base), r_mul, r_sh) + 1 : 0;
+  if (real && j < p.npat) p.walk[(size_t)item * p.npat + j] = wk;
+  int tiles = (int)(((uint32_t)wk.n + kDecTile - 1) / kDecTile);
+  for (int d = 1; d < p.lanes; d <<= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
   // an item without rows keeps one empty tile: the warp that has it writes its zeros
   hd.tiles = max(tiles, 1);
-  p.head[item] = hd;
+  if (real && j == 0) p.head[item] = hd;
   return hd.tiles;
 }
 
@@ -246,67 +246,98 @@ __device__ __forceinline__ long long block_scan(long long x, long long* s_warp) 
 // A block for each group of items.
 __global__ void __launch_bounds__(kWalkThreads)
     decode_walks_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ long long s_warp[2][kWalkThreads / 32];
-  __shared__ long long s_run[2];
+  __shared__ long long s_warp[kWalkThreads / 32];
+  __shared__ int s_tiles[kWalkThreads];
+  __shared__ long long s_run;
+  grid_dependency_wait();
   grid_dependency_release();
+  const int per = kWalkThreads / p.lanes, mine = threadIdx.x / p.lanes;  // items at a time
   const long long first = (long long)blockIdx.x * p.group;
   const int end = (int)min(first + p.group, (long long)p.items);
   long long run = 0;
-  for (int i = (int)first, k = 0; i < end; i += kWalkThreads, k ^= 1) {
-    const int item = i + threadIdx.x;
-    const long long x = run + block_scan(item < end ? describe_item(p, item) : 0, s_warp[k]);
-    if (item < end) p.upto[item] = x;
-    if (threadIdx.x == kWalkThreads - 1) s_run[k] = x;
+  for (int i = (int)first; i < end; i += per) {
+    const int tiles = describe_item(p, i + mine);
+    if ((threadIdx.x & (p.lanes - 1)) == 0) s_tiles[mine] = tiles;
     __syncthreads();
-    run = s_run[k];
+    const int item = i + threadIdx.x;
+    const bool real = threadIdx.x < per && item < end;
+    const long long x = run + block_scan(real ? s_tiles[threadIdx.x] : 0, s_warp);
+    if (real) p.upto[item] = x;
+    if (threadIdx.x == kWalkThreads - 1) s_run = x;
+    __syncthreads();
+    run = s_run;
   }
   if (threadIdx.x == 0) p.sums[blockIdx.x] = run;
 }
 
-// One block. `describe`: it describes the items itself (one a thread, a group each).
-__global__ void __launch_bounds__(kPlanThreads)
-    decode_plan_kernel(const __grid_constant__ DecodeParams p, int describe) {
-  __shared__ long long s_sum[kPlanThreads];  // inclusive sums over groups
+// One cluster; each block has a stretch of the groups. With p.group = 1 the
+// blocks describe the items themselves.
+__global__ void __cluster_dims__(kPlanBlocks) __launch_bounds__(kPlanThreads)
+    decode_plan_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ long long s_sum[kPlanThreads];  // inclusive sums over the block's groups
+  __shared__ int s_tiles[kPlanThreads];
   __shared__ long long s_warp[kPlanThreads / 32];
+  __shared__ long long s_block[kPlanBlocks];  // every block's sum
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  grid_dependency_wait();
   grid_dependency_release();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank();
   const int groups = (int)(((long long)p.items + p.group - 1) / p.group);
+  const int per = (groups + kPlanBlocks - 1) / kPlanBlocks;
+  const int g0 = rank * per, g1 = min(g0 + per, groups), cnt = max(g1 - g0, 0);
   long long x = 0;
-  if (describe) {
-    if (tid < groups) x = describe_item(p, tid);
-  } else {
-    grid_dependency_wait();
-    if (tid < groups) x = p.sums[tid];
+  if (p.group == 1) {
+    const int at_once = kPlanThreads / p.lanes, mine = tid / p.lanes;
+    for (int i = 0; i < cnt; i += at_once) {
+      const bool real = i + mine < cnt;
+      const int tiles = describe_item(p, real ? g0 + i + mine : p.items);
+      if (real && (tid & (p.lanes - 1)) == 0) s_tiles[i + mine] = tiles;
+    }
+    __syncthreads();
+    if (tid < cnt) x = s_tiles[tid];
+  } else if (tid < cnt) {
+    x = p.sums[g0 + tid];
   }
-  s_sum[tid] = block_scan(x, s_warp);
-  __syncthreads();
-  const long long total = s_sum[groups - 1];
+  x = block_scan(x, s_warp);
+  s_sum[tid] = x;
+  cluster.sync();  // the other blocks' shared memory is there
+  if (tid == kPlanThreads - 1)
+    for (int k = 0; k < kPlanBlocks; ++k) *cluster.map_shared_rank(&s_block[rank], k) = x;
+  cluster.sync();
+  long long total = 0, begin = 0;
+#pragma unroll
+  for (int k = 0; k < kPlanBlocks; ++k) {
+    if (k == rank) begin = total;
+    total += s_block[k];
+  }
+  const long long stop = begin + s_block[rank];
   const int n = (int)min((long long)p.warps, (total + p.least - 1) / p.least);
   const long long each = total / n, more = total - each * n;
   for (int k = tid; k <= p.warps; k += kPlanThreads) {
-    DecodeRange rg{-1, 0, 0, 0};
-    if (k < n) {
-      const long long t0 = each * k + min((long long)k, more);
-      int a = 0, e = groups - 1;  // first group whose inclusive sum is above t0
-      while (a < e) {
-        const int m = (a + e) >> 1;
-        if (s_sum[m] > t0) e = m; else a = m + 1;
-      }
-      long long at = a > 0 ? s_sum[a - 1] : 0;
-      rg.item = a;
-      if (p.group > 1) {  // and in it the first such item
-        const int first = a * p.group;
-        int lo = first, hi = (int)min((long long)first + p.group, (long long)p.items) - 1;
-        while (lo < hi) {
-          const int m = (int)(((long long)lo + hi) >> 1);
-          if (at + p.upto[m] > t0) hi = m; else lo = m + 1;
-        }
-        if (lo > first) at += p.upto[lo - 1];
-        rg.item = lo;
-      }
-      rg.tile = (int)(t0 - at);
-      rg.tiles = (int)(each + (k < more ? 1 : 0));
+    if (k >= n) {
+      if (rank == 0) p.range[k] = DecodeRange{-1, 0, 0, 0};
+      continue;
     }
+    const long long t0 = each * k + min((long long)k, more);
+    if (t0 < begin || t0 >= stop) continue;
+    int a = 0, e = cnt - 1;  // first group whose inclusive sum is above t0
+    while (a < e) {
+      const int m = (a + e) >> 1;
+      if (begin + s_sum[m] > t0) e = m; else a = m + 1;
+    }
+    long long at = begin + (a > 0 ? s_sum[a - 1] : 0);
+    DecodeRange rg{g0 + a, 0, (int)(each + (k < more ? 1 : 0)), 0};
+    if (p.group > 1) {  // and in it the first such item
+      const int first = (g0 + a) * p.group;
+      int lo = first, hi = (int)min((long long)first + p.group, (long long)p.items) - 1;
+      while (lo < hi) {
+        const int m = (int)(((long long)lo + hi) >> 1);
+        if (at + p.upto[m] > t0) hi = m; else lo = m + 1;
+      }
+      if (lo > first) at += p.upto[lo - 1];
+      rg.item = lo;
+    }
+    rg.tile = (int)(t0 - at);
     p.range[k] = rg;
   }
 }

@@ -1146,6 +1146,40 @@ int check_tokens(const void* k, const void* v, long long k_stride, long long v_s
   return DILATTN_OK;
 }
 
+// A launch that may start while the kernel before it on the stream still
+// runs; the kernel itself waits for that one's end before it reads its results.
+template <typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
+                              cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr;
+  memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int FMT>
+cudaError_t launch_cache_write(const CacheWriteParams& p, long long units, int page_size, cudaStream_t stream) {
+  if (p.tok.offsets == nullptr)
+    return launch_overlapped(cache_append_kernel<D, FMT>, dim3((unsigned)((units + 7) / 8)), 256, 0, stream, p);
+  // 64 numbers a lane
+  const int warps = std::max(1, page_size * D / 2048);
+  const dim3 grid((unsigned)((units * warps + 7) / 8));
+  const auto kernel = warps == 1   ? cache_write_kernel<D, FMT, 1>
+                      : warps == 2 ? cache_write_kernel<D, FMT, 2>
+                      : warps == 4 ? cache_write_kernel<D, FMT, 4>
+                                   : cache_write_kernel<D, FMT, D / 16>;
+  return launch_overlapped(kernel, grid, 256, 0, stream, p);
+}
+
 // Whether a written buffer overlaps a read one.
 bool any_overlap(const Span* mut, int nm, const Span* ro, int nr) {
   for (int i = 0; i < nm; ++i)
@@ -1190,18 +1224,17 @@ extern "C" int dilattn_cache_write(const void* k, const void* v, long long k_str
   p.codes[1] = reinterpret_cast<uint8_t*>(vc);
   p.scale[0] = ks;
   p.scale[1] = vs;
-  const long long slots = (long long)T / page_size + 2ll * B + 1;
-  if (slots > 0x7fffffffLL || Hkv > 65535) return DILATTN_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)slots, (unsigned)Hkv, 2);
-  if (format == DILATTN_CACHE_E4M3) {
-    if (d == 64) cache_write_kernel<64, kFmtE4M3><<<grid, 128, 0, stream>>>(p);
-    else cache_write_kernel<128, kFmtE4M3><<<grid, 128, 0, stream>>>(p);
-  } else {
-    if (d == 64) cache_write_kernel<64, kFmtInt8><<<grid, 128, 0, stream>>>(p);
-    else cache_write_kernel<128, kFmtInt8><<<grid, 128, 0, stream>>>(p);
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "cache_write_kernel launch");
+  const long long slots = offsets == nullptr ? B : (long long)T / page_size + 2ll * B + 1;
+  const double units = (double)slots * Hkv * 2;
+  if (units * 8 > 2147483647.0) return DILATTN_ERR_UNSUPPORTED;
+  cudaError_t e;
+  if (format == DILATTN_CACHE_E4M3)
+    e = d == 64 ? launch_cache_write<64, kFmtE4M3>(p, (long long)units, page_size, stream)
+                : launch_cache_write<128, kFmtE4M3>(p, (long long)units, page_size, stream);
+  else
+    e = d == 64 ? launch_cache_write<64, kFmtInt8>(p, (long long)units, page_size, stream)
+                : launch_cache_write<128, kFmtInt8>(p, (long long)units, page_size, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
   return DILATTN_OK;
 }
 
@@ -1241,14 +1274,10 @@ extern "C" int dilattn_cache_read(const void* kc, const void* vc, const float* k
   const long long pieces = (long long)T * Hkv * (d / 16);
   const dim3 grid((unsigned)std::min<long long>((pieces + 255) / 256, (long long)st->num_sms * 64),
                   1, 2);
-  if (format == DILATTN_CACHE_E4M3) {
-    if (d == 64) cache_read_kernel<64, kFmtE4M3><<<grid, 256, 0, stream>>>(p);
-    else cache_read_kernel<128, kFmtE4M3><<<grid, 256, 0, stream>>>(p);
-  } else {
-    if (d == 64) cache_read_kernel<64, kFmtInt8><<<grid, 256, 0, stream>>>(p);
-    else cache_read_kernel<128, kFmtInt8><<<grid, 256, 0, stream>>>(p);
-  }
-  cudaError_t e = cudaGetLastError();
+  const auto kernel = format == DILATTN_CACHE_E4M3
+                          ? (d == 64 ? cache_read_kernel<64, kFmtE4M3> : cache_read_kernel<128, kFmtE4M3>)
+                          : (d == 64 ? cache_read_kernel<64, kFmtInt8> : cache_read_kernel<128, kFmtInt8>);
+  const cudaError_t e = launch_overlapped(kernel, grid, 256, 0, stream, p);
   if (e != cudaSuccess) return cuda_fail(e, "cache_read_kernel launch");
   return DILATTN_OK;
 }
@@ -1277,45 +1306,20 @@ DecodeScratch decode_scratch(int T, int H, int Hkv, int d) {
   s.head = align256(items * sizeof(DecodeHead));
   s.walk = align256(items * kMaxPat * sizeof(DecodeWalk));
   s.upto = align256(items * 8);
-  s.sums = align256(kPlanThreads * 8);
+  s.sums = align256((size_t)kPlanBlocks * kPlanThreads * 8);
   s.range = align256((warps + 1) * sizeof(DecodeRange));
   s.part = align256(warps * 2 * std::min(G, decode_heads(G)) * (d + 4) * 4);
   return s;
 }
 
-// A launch that may start while the kernel before it on the stream still
-// runs; the kernel itself waits for that one's end before it reads its results.
-template <typename... Args>
-cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
-                              cudaStream_t stream, Args... args) {
-  cudaLaunchAttribute attr;
-  memset(&attr, 0, sizeof(attr));
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int D, int HEADS, int FMT>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   const int groups = (int)(((long long)p.items + p.group - 1) / p.group);
-  cudaError_t e;
-  if (p.group == 1) {
-    decode_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, 1);
-    e = cudaGetLastError();
-  } else {
-    decode_walks_kernel<<<groups, kWalkThreads, 0, stream>>>(p);
-    e = cudaGetLastError();
-    if (e == cudaSuccess)
-      e = launch_overlapped(decode_plan_kernel, dim3(1), kPlanThreads, 0, stream, p, 0);
-  }
+  cudaError_t e = cudaSuccess;
+  if (p.group > 1)
+    e = launch_overlapped(decode_walks_kernel, dim3((unsigned)groups), kWalkThreads, 0, stream, p);
+  if (e == cudaSuccess)
+    e = launch_overlapped(decode_plan_kernel, dim3(kPlanBlocks), kPlanThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(decode_kernel<D, HEADS, FMT>, dim3((unsigned)(p.warps / kDecWarps)),
                         kDecWarps * 32, 0, stream, p);
@@ -1437,11 +1441,12 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   divisor_magic((uint32_t)p.per_token, p.pt_mul, p.pt_sh);
   divisor_magic((uint32_t)p.nsub, p.ns_mul, p.ns_sh);
   p.items = (int)decode_items(T, Hkv, p.G);
-  // up to kPlanThreads groups, which one block sums; one item each while they last
-  p.group = p.items <= kPlanThreads
-                ? 1
-                : kWalkThreads * (int)((p.items + (long long)kWalkThreads * kPlanThreads - 1) /
-                                       ((long long)kWalkThreads * kPlanThreads));
+  // the plan's cluster has room for kPlanBlocks * kPlanThreads groups: one item each while they
+  // last, which it describes itself, else a block's worth each
+  constexpr long long most = (long long)kPlanBlocks * kPlanThreads;
+  p.group = p.items <= most ? 1 : 64 * (int)((p.items + 64 * most - 1) / (64 * most));
+  p.lanes = 1;
+  while (p.lanes < npat) p.lanes *= 2;
   const DecodeScratch lay = decode_scratch(T, H, Hkv, d);
   char* at = reinterpret_cast<char*>(workspace);
   auto take = [&at](size_t n) { return at += n, at - n; };

@@ -60,7 +60,7 @@ def test_it_makes_the_call_that_python_makes(fmt):
     # a refusal of the library comes back as its status
     small = torch.empty(256, dtype=torch.uint8, device="cuda")
     assert calls.decode(*dev, table, q, at, [(32, 1)], None, None, None, small)[0] == 4
-    with pytest.raises(dilattn.DilattnError, match="workspace"):
+    with pytest.raises(dilattn.DilattnError, match="WORKSPACE"):
         dilattn.decode(q, dev, table, at, [(32, 1)], workspace=small)
     assert dilattn.device_error() == 0
 

@@ -14,8 +14,8 @@
 // walk ends there; what overlap remains (r that do not divide one another) is
 // masked row by row. An item's walks, in tiles of 32 rows, are its work.
 //
-// Split. The tiles of all items form one sequence that is cut into equal
-// contiguous ranges, one for each warp of a persistent grid, wherever the cut
+// Split. The tiles of all items form one sequence that is cut into contiguous
+// ranges of equal weight, one for each warp of a persistent grid, wherever the cut
 // falls: no batch shape, length or head count leaves SMs idle. Warps do not
 // wait for one another. An item inside one range is finished by its warp; an
 // item that is cut leaves partials that decode_join_kernel combines in warp
@@ -41,9 +41,18 @@ constexpr int kPlanBlocks = 8;       // blocks of the plan's cluster
 constexpr int kPlanThreads = 512;    // most groups of items that one of them has
 constexpr int kWalkThreads = 256;
 
-// A warp's range of the tile sequence: its first tile is tile `tile` of item `item`.
-struct __align__(16) DecodeRange {
-  int item, tile, tiles, pad;
+// What a warp's time goes by, in quarters of a tile whose rows lie side by side:
+// a tile of spread rows (r > 1) takes 1.26 to 1.36 times as long at d = 64 and
+// 1.21 to 1.39 times at d = 128, the beginning of an item 0.7 and 0.5 of a tile (a
+// least-squares fit over the warps of ragged batches with 5 and 7 patterns).
+constexpr int kTileWeight = 4, kSpreadWeight = 5, kItemWeight = 2;
+// Two cuts so far apart have the beginning of a tile between them.
+constexpr int kRangeWeight = 8;
+
+// Where a warp's range of the tile sequence begins: at tile `tile` of item `item`.
+// The range ends where the next one begins.
+struct __align__(8) DecodeRange {
+  int item, tile;
 };
 // One walk of an item: rows base + k r, k < n. s: the segment's start (the
 // largest int when no head of the item takes part); heads: bits of those that do.
@@ -75,7 +84,6 @@ struct DecodeParams {
   int group;                 // items of a group: 1, or what a block of decode_walks_kernel describes
   int lanes;                 // threads that describe an item: a power of two, at least npat
   int warps;                 // warps of the grid
-  int least;                 // fewest tiles of a range
   float qk_scale;            // log2(e) / sqrt(d)
   int npat;                  // patterns, by ascending r
   int dense;                 // one pattern with r = 1: every head takes every row of a walk
@@ -88,8 +96,8 @@ struct DecodeParams {
   // workspace
   DecodeHead* head;          // [items]
   DecodeWalk* walk;          // [items][npat]
-  long long* upto;           // [items] tiles of the item's group up to and including it
-  long long* sums;           // [groups] tiles of each group
+  long long* upto;           // [items] weight of the item's group up to and including it
+  long long* sums;           // [groups] weight of each group
   DecodeRange* range;        // [warps + 1]
   float* part;               // [warps][2]: an item that began before the range; one that goes on past it
   int part_heads, part_stride;  // heads and floats of a partial: sums [heads][D], (m, mv, l, -) [heads]
@@ -171,7 +179,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // Plan
 // ---------------------------------------------------------------------------
 
-// Writes an item's head and walks; returns its number of tiles. p.lanes threads
+// Writes an item's head and walks; returns its weight. p.lanes threads
 // of a warp work on an item, lane j of them on pattern j; all 32 take part.
 __device__ int describe_item(const DecodeParams& p, int item) {
   const bool real = item < p.items;
@@ -220,11 +228,32 @@ __device__ int describe_item(const DecodeParams& p, int item) {
     wk.n = limit > wk.base ? (int)udiv((uint32_t)(limit - 1 - wk.base), r_mul, r_sh) + 1 : 0;
   if (real && j < p.npat) p.walk[(size_t)item * p.npat + j] = wk;
   int tiles = (int)(((uint32_t)wk.n + kDecTile - 1) / kDecTile);
-  for (int d = 1; d < p.lanes; d <<= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+  int weight = tiles * (r == 1 ? kTileWeight : kSpreadWeight);
+  for (int d = 1; d < p.lanes; d <<= 1) {
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+    weight += __shfl_xor_sync(0xffffffffu, weight, d);
+  }
   // an item without rows keeps one empty tile: the warp that has it writes its zeros
   hd.tiles = max(tiles, 1);
   if (real && j == 0) p.head[item] = hd;
-  return hd.tiles;
+  return kItemWeight + max(weight, kTileWeight);
+}
+
+// The first tile of an item that begins at or after this weight of it.
+__device__ __forceinline__ DecodeRange tile_at(const DecodeParams& p, int item, int at) {
+  const int tiles = p.head[item].tiles;
+  at -= kItemWeight;
+  if (at <= 0) return DecodeRange{item, 0};
+  int tile = 0;
+#pragma unroll 4
+  for (int j = 0; j < p.npat; ++j) {
+    const int n = (int)(((uint32_t)p.walk[(size_t)item * p.npat + j].n + kDecTile - 1) / kDecTile);
+    const int before = p.r[j] == 1 ? (at + kTileWeight - 1) / kTileWeight : (at + kSpreadWeight - 1) / kSpreadWeight;
+    tile += at > 0 ? min(before, n) : 0;
+    at -= n * (p.r[j] == 1 ? kTileWeight : kSpreadWeight);
+  }
+  // past the last one's beginning: the next item's first
+  return at > 0 || tile >= tiles ? DecodeRange{item + 1, 0} : DecodeRange{item, tile};
 }
 
 // Inclusive sums over a block's threads; s_warp: one slot for each warp.
@@ -247,7 +276,7 @@ __device__ __forceinline__ long long block_scan(long long x, long long* s_warp) 
 __global__ void __launch_bounds__(kWalkThreads)
     decode_walks_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ long long s_warp[kWalkThreads / 32];
-  __shared__ int s_tiles[kWalkThreads];
+  __shared__ int s_weight[kWalkThreads];
   __shared__ long long s_run;
   grid_dependency_wait();
   grid_dependency_release();
@@ -256,12 +285,12 @@ __global__ void __launch_bounds__(kWalkThreads)
   const int end = (int)min(first + p.group, (long long)p.items);
   long long run = 0;
   for (int i = (int)first; i < end; i += per) {
-    const int tiles = describe_item(p, i + mine);
-    if ((threadIdx.x & (p.lanes - 1)) == 0) s_tiles[mine] = tiles;
+    const int weight = describe_item(p, i + mine);
+    if ((threadIdx.x & (p.lanes - 1)) == 0) s_weight[mine] = weight;
     __syncthreads();
     const int item = i + threadIdx.x;
     const bool real = threadIdx.x < per && item < end;
-    const long long x = run + block_scan(real ? s_tiles[threadIdx.x] : 0, s_warp);
+    const long long x = run + block_scan(real ? s_weight[threadIdx.x] : 0, s_warp);
     if (real) p.upto[item] = x;
     if (threadIdx.x == kWalkThreads - 1) s_run = x;
     __syncthreads();
@@ -270,52 +299,61 @@ __global__ void __launch_bounds__(kWalkThreads)
   if (threadIdx.x == 0) p.sums[blockIdx.x] = run;
 }
 
-// One cluster; each block has a stretch of the groups. With p.group = 1 the
-// blocks describe the items themselves.
-__global__ void __cluster_dims__(kPlanBlocks) __launch_bounds__(kPlanThreads)
-    decode_plan_kernel(const __grid_constant__ DecodeParams p) {
+// One cluster of `BLOCKS`; each block has a stretch of the groups. With p.group = 1
+// the blocks describe the items themselves.
+template <int BLOCKS>
+__global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ long long s_sum[kPlanThreads];  // inclusive sums over the block's groups
-  __shared__ int s_tiles[kPlanThreads];
+  __shared__ int s_weight[kPlanThreads];
   __shared__ long long s_warp[kPlanThreads / 32];
-  __shared__ long long s_block[kPlanBlocks];  // every block's sum
-  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  __shared__ long long s_block[BLOCKS];  // every block's sum
+  // the other blocks' shared memory is there once this has been waited for
+  if constexpr (BLOCKS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   grid_dependency_wait();
   grid_dependency_release();
-  const int tid = threadIdx.x, rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, rank = (int)blockIdx.x;
   const int groups = (int)(((long long)p.items + p.group - 1) / p.group);
-  const int per = (groups + kPlanBlocks - 1) / kPlanBlocks;
+  const int per = (groups + BLOCKS - 1) / BLOCKS;
   const int g0 = rank * per, g1 = min(g0 + per, groups), cnt = max(g1 - g0, 0);
   long long x = 0;
   if (p.group == 1) {
     const int at_once = kPlanThreads / p.lanes, mine = tid / p.lanes;
     for (int i = 0; i < cnt; i += at_once) {
       const bool real = i + mine < cnt;
-      const int tiles = describe_item(p, real ? g0 + i + mine : p.items);
-      if (real && (tid & (p.lanes - 1)) == 0) s_tiles[i + mine] = tiles;
+      const int weight = describe_item(p, real ? g0 + i + mine : p.items);
+      if (real && (tid & (p.lanes - 1)) == 0) s_weight[i + mine] = weight;
     }
     __syncthreads();
-    if (tid < cnt) x = s_tiles[tid];
+    if (tid < cnt) x = s_weight[tid];
   } else if (tid < cnt) {
     x = p.sums[g0 + tid];
   }
   x = block_scan(x, s_warp);
   s_sum[tid] = x;
-  cluster.sync();  // the other blocks' shared memory is there
-  if (tid == kPlanThreads - 1)
-    for (int k = 0; k < kPlanBlocks; ++k) *cluster.map_shared_rank(&s_block[rank], k) = x;
-  cluster.sync();
   long long total = 0, begin = 0;
+  if constexpr (BLOCKS > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    __syncthreads();
+    if (tid < BLOCKS) {
+      cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+      *cluster.map_shared_rank(&s_block[rank], tid) = s_sum[kPlanThreads - 1];
+    }
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
-  for (int k = 0; k < kPlanBlocks; ++k) {
-    if (k == rank) begin = total;
-    total += s_block[k];
+    for (int k = 0; k < BLOCKS; ++k) {
+      if (k == rank) begin = total;
+      total += s_block[k];
+    }
+  } else {
+    __syncthreads();
+    total = s_sum[kPlanThreads - 1];
   }
-  const long long stop = begin + s_block[rank];
-  const int n = (int)min((long long)p.warps, (total + p.least - 1) / p.least);
+  const long long stop = begin + s_sum[kPlanThreads - 1];
+  const int n = (int)max(min((long long)p.warps, total / kRangeWeight), 1ll);
   const long long each = total / n, more = total - each * n;
   for (int k = tid; k <= p.warps; k += kPlanThreads) {
-    if (k >= n) {
-      if (rank == 0) p.range[k] = DecodeRange{-1, 0, 0, 0};
+    if (k >= n) {  // ends of the last range, and empty ones
+      if (rank == 0) p.range[k] = DecodeRange{p.items, 0};
       continue;
     }
     const long long t0 = each * k + min((long long)k, more);
@@ -326,19 +364,18 @@ __global__ void __cluster_dims__(kPlanBlocks) __launch_bounds__(kPlanThreads)
       if (begin + s_sum[m] > t0) e = m; else a = m + 1;
     }
     long long at = begin + (a > 0 ? s_sum[a - 1] : 0);
-    DecodeRange rg{g0 + a, 0, (int)(each + (k < more ? 1 : 0)), 0};
+    int item = g0 + a;
     if (p.group > 1) {  // and in it the first such item
-      const int first = (g0 + a) * p.group;
+      const int first = item * p.group;
       int lo = first, hi = (int)min((long long)first + p.group, (long long)p.items) - 1;
       while (lo < hi) {
         const int m = (int)(((long long)lo + hi) >> 1);
         if (at + p.upto[m] > t0) hi = m; else lo = m + 1;
       }
       if (lo > first) at += p.upto[lo - 1];
-      rg.item = lo;
+      item = lo;
     }
-    rg.tile = (int)(t0 - at);
-    p.range[k] = rg;
+    p.range[k] = tile_at(p, item, (int)(t0 - at));
   }
 }
 
@@ -414,44 +451,55 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   const int g = lane >> 2, c = lane & 3;
   const int row_l = 8 * c + g;                     // the row this lane looks up
   const int first_slot = VR == 1 ? c : VR == 2 ? (c & 2) : 0;
+  // the lane's own fragments of Q, where registers are short
+  __shared__ uint2 s_q[kDecWarps][NB * MT * 32];
+  uint2* const qf = s_q[warp] + lane;
+  __shared__ DecodeWalk s_walk[kDecWarps][kMaxPat];  // of the item to fetch from
   // neighbouring warps of the sequence on different SMs: few ranges spread over all
   const int wi = warp * (int)gridDim.x + (int)blockIdx.x;
 
   grid_dependency_wait();
-  const DecodeRange rg = p.range[wi];
+  const DecodeRange rg = p.range[wi], end = p.range[wi + 1];
   grid_dependency_release();
-  if (rg.tiles == 0) return;
+  if (rg.item == end.item && rg.tile == end.tile) return;
 
   const int pmask = (1 << p.geom.lp) - 1;
 
   // ---- the walk to fetch from (a_...), the looked-up tile (f_...), the tile in registers
-  DecodeWalk aw;             // lane j: pattern j's walk of the item
-  int a_item = rg.item, a_left = rg.tiles, a_pos, a_hk, a_j, a_n, a_base, a_r;
-  uint32_t a_k, a_in;        // a_in: patterns of the item's head (HEADS = 1)
-  const int* a_table;
+  int a_item = rg.item, a_tiles, a_pos, a_hk, a_b, a_j, a_n, a_base, a_r;  // a_tiles: of the item, in the range
+  uint32_t a_k, a_walks, a_in;  // patterns with rows to walk; patterns of the item's head (HEADS = 1)
   int f_page = -1, f_x = 0, f_hk = 0;
   uint32_t f_meta = 0;
-  bool f_some = false, f_whole = false;
+  bool a_some = true, f_some = false, f_whole = false;
 
   auto set_walk = [&](int j) {
+    const DecodeWalk wk = s_walk[warp][j];
     a_j = j;
-    a_n = __shfl_sync(0xffffffffu, aw.n, j);
-    a_base = __shfl_sync(0xffffffffu, aw.base, j);
+    a_n = wk.n;
+    a_base = wk.base;
     a_r = p.r[j];
   };
-  auto load_walks = [&](int item) {
-    aw = DecodeWalk{0x7fffffff, 0, 0, 0u};
-    if (lane < p.npat) aw = p.walk[(size_t)item * p.npat + lane];
+  auto load_walks = [&](int item) {  // returns this lane's
+    DecodeWalk wk{0x7fffffff, 0, 0, 0u};
+    if (lane < p.npat) wk = p.walk[(size_t)item * p.npat + lane];
     const DecodeHead hd = p.head[item];
     a_pos = hd.pos;
-    a_table = p.geom.table + (size_t)hd.b * p.geom.max_pages;
-    const DecodeItem it = item_of(p, item);
-    a_hk = it.hk;
-    a_in = __ballot_sync(0xffffffffu, aw.heads & 1u);
+    a_b = hd.b;
+    a_hk = item_of(p, item).hk;
+    a_tiles = item == end.item ? end.tile : hd.tiles;
+    a_walks = __ballot_sync(0xffffffffu, wk.n > 0);
+    a_in = __ballot_sync(0xffffffffu, wk.heads & 1u);
+    if (lane < kMaxPat) s_walk[warp][lane] = wk;
+    __syncwarp();
+    return wk;
+  };
+  auto first_walk = [&]() {
+    set_walk(a_walks != 0 ? __ffs(a_walks) - 1 : 0);
+    a_k = 0;
   };
   // look up the pages of the next tile's rows
   auto look_up = [&]() {
-    f_some = a_left > 0;
+    f_some = a_some;
     if (!f_some) return;
     const uint32_t k = a_k + row_l, n = (uint32_t)a_n;  // k may pass 2^31 in the last tile
     f_hk = a_hk;
@@ -461,7 +509,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
     f_whole = a_r == 1 && a_k + kDecTile <= n && (x0 & pmask) + kDecTile <= pmask + 1;
     if (k < n) {
       f_x = x0 + row_l * a_r;
-      f_page = a_table[f_x >> p.geom.lp];
+      f_page = p.geom.table[(size_t)a_b * p.geom.max_pages + (f_x >> p.geom.lp)];
     }
     if (p.dense) {
       f_meta = k < n ? 0x10001u : 0u;
@@ -470,7 +518,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
       const int last = (int)((uint32_t)a_base + min(a_k + kDecTile - 1, n - 1) * (uint32_t)a_r);
       uint32_t held = 1u << a_j;
       for (int i = 0; i < p.npat; ++i) {
-        const int si = __shfl_sync(0xffffffffu, aw.s, i);
+        const int si = s_walk[warp][i].s;
         if (i == a_j || last < si) continue;
         if (f_x >= si && divides(p, i, a_pos - f_x)) held |= 1u << i;
       }
@@ -482,18 +530,17 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
         f_meta = k < n ? held | upto << 16 : 0u;
       }
     }
-    --a_left;
     a_k += kDecTile;
-    if (a_k >= n) {
-      a_k = 0;
-      const uint32_t more = __ballot_sync(0xffffffffu, aw.n > 0) & ~((2u << a_j) - 1);
-      if (more != 0) {
-        set_walk(__ffs(more) - 1);
-      } else if (a_left > 0) {
+    if (--a_tiles == 0) {
+      a_some = a_item != end.item && (a_item + 1 != end.item || end.tile != 0);
+      if (a_some) {
+        __syncwarp();
         load_walks(++a_item);
-        const uint32_t any = __ballot_sync(0xffffffffu, aw.n > 0);
-        set_walk(any != 0 ? __ffs(any) - 1 : 0);
+        first_walk();
       }
+    } else if (a_k >= n) {
+      a_k = 0;
+      set_walk(__ffs(a_walks & ~((2u << a_j) - 1)) - 1);
     }
   };
   constexpr int KQ = D / 64, VW = D / 32;  // 16-byte pieces of a K row, words of a V row, that a lane holds
@@ -557,15 +604,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   };
 
   // ---- the item in hand
-  DecodeItem it;
-  int tiles;                 // its tiles from here on
+  int tiles;                 // its tiles from here on, in the range
   float acc[MT][NB][4];
   float m[2 * NB], mv[2 * NB], l[2 * NB], fac[2 * NB];  // of columns nb * 8 + 2 c + e
-  uint32_t qf[NB][MT][2];
   uint32_t in_pat[2 * NB];   // patterns that each of the lane's heads takes part in
   auto begin_item = [&](int item) {
-    it = item_of(p, item);
-    tiles = p.head[item].tiles;
+    const DecodeItem it = item_of(p, item);
+    tiles = item == end.item ? end.tile : p.head[item].tiles;
     const uint32_t heads = lane < p.npat ? p.walk[(size_t)item * p.npat + lane].heads : 0u;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -599,8 +644,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
                                             __uint_as_float(raw[k].x & 0xffff0000u) * f1 * f2);
         const __half2 b = __floats2half2_rn(__uint_as_float(raw[k].y << 16) * f1 * f2,
                                             __uint_as_float(raw[k].y & 0xffff0000u) * f1 * f2);
-        qf[nb][k][0] = *reinterpret_cast<const uint32_t*>(&a);
-        qf[nb][k][1] = *reinterpret_cast<const uint32_t*>(&b);
+        qf[(nb * MT + k) * 32] = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
       }
       const float down = big >= 0x7f80u ? __uint_as_float(0x7fffffffu)  // NaN or infinity in q
                                         : p.qk_scale / f1 / f2;
@@ -629,8 +674,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   // where a lane's sums of one of its heads lie: d = g (D / 8) + 0 .. D / 8 - 1
   auto sum_of = [&](int nb, int e, int k) { return acc[k >> 1][nb][(k & 1) * 2 + e]; };
 
-  // The item is done here (dst null: this warp had all of it), or a partial of it goes to dst.
-  auto end_item = [&](float* dst) {
+  // The item is done here (slot < 0: this warp had all of it), or a partial of it goes to the slot.
+  auto end_item = [&](int item, int slot) {
+    const DecodeItem it = item_of(p, item);
+    float* const dst = p.part + ((size_t)wi * 2 + max(slot, 0)) * p.part_stride;
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i) {
 #pragma unroll
@@ -643,7 +690,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
       for (int e = 0; e < VE; ++e) {
         const int i = 2 * nb + e, hl = nb * 8 + 2 * c + e;
         if (hl >= it.nh) continue;
-        if (dst == nullptr) {
+        if (slot < 0) {
           const float f = final_factor(m[i], mv[i], l[i]);
           const size_t oi = (size_t)it.token * p.H + it.h0 + hl;
           uint32_t o[D / 16];
@@ -672,30 +719,32 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   };
 
   // ---- start: the walk that the first tile belongs to
-  load_walks(a_item);
-  {
-    uint32_t end = ((uint32_t)aw.n + kDecTile - 1) / kDecTile;
+  const DecodeWalk wk = load_walks(a_item);
+  a_tiles -= rg.tile;
+  if (rg.tile == 0) {
+    first_walk();
+  } else {
+    uint32_t past = ((uint32_t)wk.n + kDecTile - 1) / kDecTile;  // tiles of walks up to this lane's
 #pragma unroll
     for (int s = 1; s < kMaxPat; s <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, end, s);
-      if (lane >= s) end += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, past, s);
+      if (lane >= s) past += y;
     }
-    const int j = min(__popc(__ballot_sync(0xffffffffu, lane < p.npat && (uint32_t)rg.tile >= end)), p.npat - 1);
-    const uint32_t before = j > 0 ? __shfl_sync(0xffffffffu, end, j - 1) : 0u;
+    const int j = __popc(__ballot_sync(0xffffffffu, lane < p.npat && (uint32_t)rg.tile >= past));
+    const uint32_t before = j > 0 ? __shfl_sync(0xffffffffu, past, j - 1) : 0u;
     set_walk(j);
     a_k = ((uint32_t)rg.tile - before) * kDecTile;
   }
   look_up();
+  int item = rg.item;
+  bool from_start = rg.tile == 0;
+  begin_item(item);  // its loads go with the first tile's page numbers
+  tiles -= rg.tile;
   resolve();
   load_k();
   load_v();
   look_up();
-  int item = rg.item;
-  bool from_start = rg.tile == 0;
-  begin_item(item);
-  tiles -= rg.tile;
-  float* const part = p.part + (size_t)wi * 2 * p.part_stride;
-  for (int left = rg.tiles; left > 0; --left) {
+  for (bool more = true; more;) {
     // ---- scores: block rb's rows g and g + 8, columns nb * 8 + 2 c and + 1
     float sc[2][NB][4];
 #pragma unroll
@@ -707,17 +756,20 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
 #pragma unroll
     for (int q = 0; q < KQ; ++q)
 #pragma unroll
-      for (int rb = 0; rb < 2; ++rb) {
-        const uint4 ka = kr[2 * rb][q], kb = kr[2 * rb + 1][q];
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+      for (int k = 0; k < 4; ++k) {
+        uint2 qk[NB];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int nb = 0; nb < NB; ++nb) qk[nb] = qf[(nb * MT + q * 4 + k) * 32];
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb) {
+          const uint4 ka = kr[2 * rb][q], kb = kr[2 * rb + 1][q];
+          const uint32_t wa = k == 0 ? ka.x : k == 1 ? ka.y : k == 2 ? ka.z : ka.w;
+          const uint32_t wb = k == 0 ? kb.x : k == 1 ? kb.y : k == 2 ? kb.z : kb.w;
           uint32_t a0, a1, a2, a3;
-          codes_to_half<FMT>(wa[k], a0, a2);
-          codes_to_half<FMT>(wb[k], a1, a3);
+          codes_to_half<FMT>(wa, a0, a2);
+          codes_to_half<FMT>(wb, a1, a3);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma_16816(sc[rb][nb], a0, a1, a2, a3, qf[nb][q * 4 + k][0], qf[nb][q * 4 + k][1]);
+          for (int nb = 0; nb < NB; ++nb) mma_16816(sc[rb][nb], a0, a1, a2, a3, qk[nb].x, qk[nb].y);
         }
       }
     // ---- what the softmax needs of the lane's rows (slots first_slot ..); then the next tile
@@ -737,7 +789,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
         if (VR > 1 && !(whole && p.dense)) meta[v] = __shfl_sync(0xffffffffu, meta_l, from);
       }
     }
-    if (left > 1) {
+    more = f_some;
+    if (more) {
       resolve();
       load_k();
       look_up();
@@ -858,10 +911,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
               mma_16816(acc[2 * k + half][nb], a0, a1, a2, a3, pf[rb][nb][0], pf[rb][nb][1]);
           }
     }
-    if (left > 1) load_v();
-    if (--tiles == 0 || left == 1) {
-      end_item(!from_start ? part : tiles > 0 ? part + p.part_stride : nullptr);
-      if (left > 1) {
+    if (more) load_v();
+    if (--tiles == 0) {
+      end_item(item, !from_start ? 0 : item == end.item ? 1 : -1);
+      if (more) {
         from_start = true;
         begin_item(++item);
       }
@@ -919,16 +972,25 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   const size_t step = (size_t)2 * p.part_stride;
   const int so = p.part_heads * D + hl * 4;
   if (tid == 0) s_long = -1;
+  // The ranges are there: this kernel was let start after every block of the main one had waited
+  // for the plan. What other kernels left of them in L1 is passed over.
+  const int w_own = w0 + warp;
+  DecodeRange a{0, 0}, b{0, 0}, r{-1, 0};  // r: ranges w_own + 1 .., those that hold a part of the item
+  if (w_own < p.warps) {
+    const int2 x = __ldcg(reinterpret_cast<const int2*>(p.range + w_own));
+    const int2 y = __ldcg(reinterpret_cast<const int2*>(p.range + w_own + 1));
+    a = DecodeRange{x.x, x.y}, b = DecodeRange{y.x, y.y};
+    if (w_own + 1 + lane < p.warps)
+      r.item = __ldcg(reinterpret_cast<const int2*>(p.range + w_own + 1 + lane)).x;
+  }
   grid_dependency_wait();
   __syncthreads();
-  if (const int w = w0 + warp; w < p.warps) {
-    const DecodeRange a = p.range[w], b = p.range[w + 1];
-    DecodeRange r{-1, 0, 0, 0};  // ranges w + 1 ..: those that hold a part of the item
-    if (w + 1 + lane < p.warps) r = p.range[w + 1 + lane];
-    const DecodeItem it = item_of(p, max(b.item, 0));
+  {
+    const int w = w_own;
+    const DecodeItem it = item_of(p, b.tile > 0 ? b.item : 0);
     // an item begins in range w and goes on past it
-    if (b.tiles > 0 && b.tile > 0 && (a.item != b.item || a.tile == 0) && hl < it.nh) {
-      const uint32_t held = __ballot_sync(0xffffffffu, r.tiles > 0 && r.item == b.item);
+    if (b.tile > 0 && (a.item != b.item || a.tile == 0) && hl < it.nh) {
+      const uint32_t held = __ballot_sync(0xffffffffu, r.item == b.item);
       if (held == 0xffffffffu) {
         if (lane == 0) s_long = w;
       } else {
@@ -971,10 +1033,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   float2 top = *reinterpret_cast<const float2*>(first + so);
   for (int k = 1 + tid;; k += kJoinThreads) {
     bool mine = w + k < p.warps;
-    if (mine) {
-      const DecodeRange r = p.range[w + k];
-      mine = r.tiles > 0 && r.item == item;
-    }
+    if (mine) mine = p.range[w + k].item == item;
     if (mine) {
       const float2 f = *reinterpret_cast<const float2*>(rest + k * step + so);
       top.x = fmaxf(top.x, f.x);

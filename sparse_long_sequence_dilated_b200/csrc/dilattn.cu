@@ -1148,21 +1148,24 @@ int check_tokens(const void* k, const void* v, long long k_stride, long long v_s
 
 // A launch that may start while the kernel before it on the stream still
 // runs; the kernel itself waits for that one's end before it reads its results.
-template <typename... Args>
+template <int CLUSTER = 1, typename... Args>
 cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
                               cudaStream_t stream, Args... args) {
-  cudaLaunchAttribute attr;
-  memset(&attr, 0, sizeof(attr));
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  memset(attr, 0, sizeof(attr));
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CLUSTER;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1319,7 +1322,10 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   if (p.group > 1)
     e = launch_overlapped(decode_walks_kernel, dim3((unsigned)groups), kWalkThreads, 0, stream, p);
   if (e == cudaSuccess)
-    e = launch_overlapped(decode_plan_kernel, dim3(kPlanBlocks), kPlanThreads, 0, stream, p);
+    e = groups <= kPlanThreads / p.lanes && p.group == 1
+            ? launch_overlapped(decode_plan_kernel<1>, dim3(1), kPlanThreads, 0, stream, p)
+            : launch_overlapped<kPlanBlocks>(decode_plan_kernel<kPlanBlocks>, dim3(kPlanBlocks), kPlanThreads, 0,
+                                             stream, p);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(decode_kernel<D, HEADS, FMT>, dim3((unsigned)(p.warps / kDecWarps)),
                         kDecWarps * 32, 0, stream, p);
@@ -1463,10 +1469,8 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   double rows = 0;
   for (int i = 0; i < npat; ++i) rows += (double)std::min<long long>(w[i], longest) / r[i] + 1;
   const double tiles = (rows / kDecTile + npat) * p.items;
-  p.least = 2;
   const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(p.G, d);
-  p.warps = kDecWarps * (int)std::min<double>(blocks, tiles / (kDecWarps * p.least) + 1);
-  if (tiles / p.warps > 2147483647.0) return DILATTN_ERR_UNSUPPORTED;  // a range's tiles are an int
+  p.warps = kDecWarps * (int)std::min<double>(blocks, tiles * kSpreadWeight / (kDecWarps * kRangeWeight) + 1);
   cudaError_t e;
   if (format == DILATTN_CACHE_E4M3)
     e = d == 64 ? launch_decode_heads<64, kFmtE4M3>(p, stream) : launch_decode_heads<128, kFmtE4M3>(p, stream);

@@ -154,59 +154,127 @@ __device__ __forceinline__ void rescale_rows(uint8_t* codes, int P, int r0, int 
   }
 }
 
-// One token of each sequence: a warp for each (sequence, KV head, K or V).
+// The new rows of a page slot: rows r0 .. r0 + rows - 1 of `page`, from token
+// `tok` on; rows = 0 when the slot has none. The same in all lanes of a warp.
+// A sequence of n tokens touches at most floor(n / P) + 2 pages: sequence b, whose
+// first token is off, owns the slots from floor(off / P) + 2 b up to the next one's.
+struct PageRows {
+  int page, r0, rows, tok;
+};
+__device__ __forceinline__ PageRows page_rows(const CacheWriteParams& p, long long slot) {
+  const int lane = threadIdx.x & 31, P = 1 << p.geom.lp;
+  PageRows pr{0, 0, 0, 0};
+  int b = 0, off, n, start;
+  if (p.tok.offsets != nullptr) {
+    // the slot's sequence: the last one whose first slot is at or before it
+    for (int span = p.geom.B;;) {
+      const int step = (span + 31) / 32, at = b + lane * step;
+      int lo = 0, len = 0, st = 0;
+      if (lane * step < span) {
+        token_range(p.tok, at, lo, len);
+        if (step == 1) st = p.tok.start[at];
+      }
+      const bool in = lane * step < span && (lo >> p.geom.lp) + 2ll * at <= slot;
+      const int k = max(__popc(__ballot_sync(0xffffffffu, in)) - 1, 0);
+      b += k * step;
+      if (step == 1) {
+        off = __shfl_sync(0xffffffffu, lo, k);
+        n = __shfl_sync(0xffffffffu, len, k);
+        start = __shfl_sync(0xffffffffu, st, k);
+        break;
+      }
+      span = min(step, span - k * step);
+    }
+  } else {
+    b = (int)min(slot, (long long)p.geom.B - 1);
+    token_range(p.tok, b, off, n);
+    start = p.tok.start[b];
+  }
+  if (n == 0) return pr;
+  if (start < 0 || start > 0x7fffffff - n) {
+    p.geom.err.raise(kErrBadPage);
+    return pr;
+  }
+  const long long skip = slot - (p.tok.offsets != nullptr ? (off >> p.geom.lp) + 2ll * b : b);
+  const long long row0 = ((long long)(start >> p.geom.lp) + skip) << p.geom.lp;
+  const long long lo = max((long long)start, row0), hi = min((long long)start + n, row0 + P);
+  if (lo >= hi) return pr;
+  const int page = page_of(p.geom, b, (int)lo);
+  if (page < 0) return pr;
+  pr.page = page;
+  pr.r0 = (int)(lo - row0);
+  pr.rows = (int)(hi - lo);
+  pr.tok = off + (int)(lo - start);
+  return pr;
+}
+
+// Few tokens of each sequence: a warp for each (touched page, KV head, K or V).
+// A page's first four new rows stay in registers, others are read twice.
 template <int D, int FMT>
 __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant__ CacheWriteParams p) {
-  constexpr int C = D / 64;  // 32-bit words of two numbers that a lane has
+  constexpr int C = D / 64;  // 32-bit words of two numbers that a lane has of a row
+  constexpr int KEEP = 4;
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int h = (int)(unit % p.geom.Hkv);
-  const int z = (int)(unit / p.geom.Hkv) & 1, b = (int)(unit / p.geom.Hkv >> 1);
+  const int z = (int)(unit / p.geom.Hkv) & 1;
   grid_dependency_wait();
-  if (b >= p.geom.B) return;
-  const int pos = p.tok.start[b];
-  if (pos < 0) {
-    p.geom.err.raise(kErrBadPage);
-    return;
-  }
-  uint32_t x[C];
-  const uint32_t* src = reinterpret_cast<const uint32_t*>(p.x[z] + (long long)b * p.stride[z] + (long long)h * D);
-  if constexpr (C == 2) {
-    const uint2 u = reinterpret_cast<const uint2*>(src)[lane];
-    x[0] = u.x, x[1] = u.y;
-  } else {
-    x[0] = src[lane];
-  }
-  const int page = page_of(p.geom, b, pos);
-  if (page < 0) return;
-  const int row = pos & ((1 << p.geom.lp) - 1);
-  uint8_t* codes = p.codes[z] + (((size_t)page * p.geom.Hkv + h) << p.geom.lp) * D;
-  float* scale = p.scale[z] + (size_t)page * p.geom.Hkv + h;
-  const float was = row == 0 ? 0.f : *scale;
-  uint32_t amax = 0;
+  grid_dependency_release();
+  const PageRows pr = page_rows(p, unit / p.geom.Hkv >> 1);
+  if (pr.rows == 0) return;
+  const __nv_bfloat16* x = p.x[z] + (long long)pr.tok * p.stride[z] + (long long)h * D;
+  const size_t blk = (size_t)pr.page * p.geom.Hkv + h;
+  uint8_t* codes = p.codes[z] + (blk << p.geom.lp) * D;
+  float* scale = p.scale[z] + blk;
+  auto load = [&](int i, uint32_t (&u)[C]) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(x + (long long)i * p.stride[z]);
+    if constexpr (C == 2) {
+      const uint2 v = reinterpret_cast<const uint2*>(src)[lane];
+      u[0] = v.x, u[1] = v.y;
+    } else {
+      u[0] = src[lane];
+    }
+  };
+  const float was = pr.r0 == 0 ? 0.f : *scale;
+  uint32_t kept[KEEP][C], amax = 0;
 #pragma unroll
-  for (int i = 0; i < C; ++i) amax = max(max(amax, x[i] & 0x7fffu), (x[i] >> 16) & 0x7fffu);
+  for (int i = 0; i < KEEP; ++i) {
+#pragma unroll
+    for (int k = 0; k < C; ++k) kept[i][k] = 0;
+    if (i < pr.rows) load(i, kept[i]);
+  }
+  auto take = [&](const uint32_t (&u)[C]) {
+#pragma unroll
+    for (int k = 0; k < C; ++k) amax = max(max(amax, u[k] & 0x7fffu), (u[k] >> 16) & 0x7fffu);
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) take(kept[i]);
+  for (int i = KEEP; i < pr.rows; ++i) {
+    uint32_t u[C];
+    load(i, u);
+    take(u);
+  }
   const float now = next_scale<FMT>(__reduce_max_sync(0xffffffffu, amax), was);
   const bool poisoned = now != now;
   const float inv = poisoned ? 0.f : 1.f / now;
-  if (row != 0 && now > was) rescale_rows<D, FMT>(codes, 1 << p.geom.lp, row, row + 1, was * inv, lane, 32);
-  if (poisoned)
+  if (pr.r0 > 0 && now > was) rescale_rows<D, FMT>(codes, 1 << p.geom.lp, pr.r0, pr.r0 + pr.rows, was * inv, lane, 32);
+  auto store = [&](int i, uint32_t (&u)[C]) {
+    if (poisoned)
 #pragma unroll
-    for (int i = 0; i < C; ++i) x[i] = 0;
-  if constexpr (C == 2) {
-    reinterpret_cast<uint32_t*>(codes + (size_t)row * D)[lane] = encode_bf16x4<FMT>(x[0], x[1], inv);
-  } else {
-    reinterpret_cast<uint16_t*>(codes + (size_t)row * D)[lane] = (uint16_t)encode_bf16x4<FMT>(x[0], 0u, inv);
+      for (int k = 0; k < C; ++k) u[k] = 0;
+    uint8_t* dst = codes + (size_t)(pr.r0 + i) * D;
+    if constexpr (C == 2) reinterpret_cast<uint32_t*>(dst)[lane] = encode_bf16x4<FMT>(u[0], u[1], inv);
+    else reinterpret_cast<uint16_t*>(dst)[lane] = (uint16_t)encode_bf16x4<FMT>(u[0], 0u, inv);
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i)
+    if (i < pr.rows) store(i, kept[i]);
+  for (int i = KEEP; i < pr.rows; ++i) {
+    uint32_t u[C];
+    load(i, u);
+    store(i, u);
   }
   if (lane == 0) *scale = now;
-}
-
-// First page slot of sequence b. A sequence of n tokens touches at most
-// floor(n / P) + 2 pages, so it owns the slots up to the next sequence's first.
-__device__ __forceinline__ long long first_slot_of(const CacheWriteParams& p, int b) {
-  int lo, n;
-  token_range(p.tok, b, lo, n);
-  return (lo >> p.geom.lp) + 2ll * b;
 }
 
 // Ragged stretches: W warps for each (touched page, KV head, K or V), with all
@@ -221,37 +289,14 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant_
   const long long unit = (long long)blockIdx.x * (8 / W) + warp / W;
   const int h = (int)(unit % p.geom.Hkv);
   const int z = (int)(unit / p.geom.Hkv) & 1;
-  const long long slot = unit / p.geom.Hkv >> 1;
   const int P = 1 << p.geom.lp;
   grid_dependency_wait();
-  // the slot's sequence: the last one whose first slot is at or before it
-  int b = 0;
-  for (int span = p.geom.B; span > 1;) {
-    const int step = (span + 31) / 32, at = b + lane * step;
-    const bool in = lane * step < span && first_slot_of(p, at) <= slot;
-    const int k = max(__popc(__ballot_sync(0xffffffffu, in)) - 1, 0);
-    b += k * step;
-    span = min(step, span - k * step);
-  }
-  int off, n;
-  token_range(p.tok, b, off, n);
-  const int start = p.tok.start[b];
-  int lo = 0, hi = 0, page = -1;
-  long long row0 = 0;
-  if (n > 0) {
-    if (start < 0 || start > 0x7fffffff - n) {
-      if (tid == 0) p.geom.err.raise(kErrBadPage);
-    } else {
-      row0 = ((long long)(start >> p.geom.lp) + slot - first_slot_of(p, b)) << p.geom.lp;
-      lo = (int)min(max((long long)start, row0), 0x7fffffffll);
-      hi = (int)min((long long)start + n, row0 + P);
-      if (lo < hi) page = page_of(p.geom, b, lo);
-    }
-  }
-  const bool work = page >= 0;
-  const __nv_bfloat16* x = p.x[z] + (long long)(off + lo - start) * p.stride[z] + (long long)h * D;
-  const int r0 = (int)(lo - row0), rows = work ? hi - lo : 0;
-  const size_t blk = work ? (size_t)page * p.geom.Hkv + h : 0;
+  grid_dependency_release();
+  const PageRows pr = page_rows(p, unit / p.geom.Hkv >> 1);
+  const bool work = pr.rows > 0;
+  const int r0 = pr.r0, rows = pr.rows;
+  const __nv_bfloat16* x = p.x[z] + (long long)pr.tok * p.stride[z] + (long long)h * D;
+  const size_t blk = (size_t)pr.page * p.geom.Hkv + h;
   uint8_t* codes = p.codes[z] + (blk << p.geom.lp) * D;
   float* scale = p.scale[z] + blk;
   uint4 u[4][2];
@@ -310,6 +355,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__
   const long long total = per * p.tok.T;
   const int z = blockIdx.z;
   grid_dependency_wait();
+  grid_dependency_release();
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (long long)gridDim.x * 256) {
     const int tok = (int)(i / per), rest = (int)(i % per);

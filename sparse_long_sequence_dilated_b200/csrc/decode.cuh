@@ -21,7 +21,7 @@
 // item that is cut leaves partials that decode_join_kernel combines in warp
 // order (no atomics: the same call gives the same bits).
 //
-// Launches: decode_plan_kernel, one cluster, describes every item's walks once
+// Launches: decode_plan_kernel, one block or cluster, describes every item's walks once
 // and cuts the sequence (above kPlanBlocks * kPlanThreads items,
 // decode_walks_kernel describes them before it, over the whole GPU), then
 // decode_kernel, then decode_join_kernel. Each is launched while the one before
@@ -38,7 +38,8 @@ constexpr int kDecWarps = 4;         // warps of a block
 constexpr int kDecMaxSms = 160;      // the workspace has partials for the warps of this many SMs
 constexpr int kDecTile = 32;         // rows of a tile
 constexpr int kPlanBlocks = 8;       // blocks of the plan's cluster
-constexpr int kPlanThreads = 512;    // most groups of items that one of them has
+constexpr int kPlanThreads = 512;    // threads of one of them, and the most groups of items that it has
+constexpr int kPlanAlone = 1024;     // threads of a plan of one block
 constexpr int kWalkThreads = 256;
 
 // What a warp's time goes by, in quarters of a tile whose rows lie side by side:
@@ -299,13 +300,20 @@ __global__ void __launch_bounds__(kWalkThreads)
   if (threadIdx.x == 0) p.sums[blockIdx.x] = run;
 }
 
+// a / b for numbers from 0 on, in 32 bits where they fit: a 64-bit division takes several times as long.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return (a | b) >> 32 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // One cluster of `BLOCKS`; each block has a stretch of the groups. With p.group = 1
 // the blocks describe the items themselves.
 template <int BLOCKS>
-__global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ long long s_sum[kPlanThreads];  // inclusive sums over the block's groups
-  __shared__ int s_weight[kPlanThreads];
-  __shared__ long long s_warp[kPlanThreads / 32];
+__global__ void __launch_bounds__(BLOCKS > 1 ? kPlanThreads : kPlanAlone)
+    decode_plan_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int THREADS = BLOCKS > 1 ? kPlanThreads : kPlanAlone;
+  __shared__ long long s_sum[THREADS];  // inclusive sums over the block's groups
+  __shared__ int s_weight[THREADS];
+  __shared__ long long s_warp[THREADS / 32];
   __shared__ long long s_block[BLOCKS];  // every block's sum
   // the other blocks' shared memory is there once this has been waited for
   if constexpr (BLOCKS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -317,8 +325,9 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const __grid_
   const int g0 = rank * per, g1 = min(g0 + per, groups), cnt = max(g1 - g0, 0);
   long long x = 0;
   if (p.group == 1) {
-    const int at_once = kPlanThreads / p.lanes, mine = tid / p.lanes;
+    const int at_once = THREADS / p.lanes, mine = tid / p.lanes;
     for (int i = 0; i < cnt; i += at_once) {
+      if (i + (tid & ~31) / p.lanes >= cnt) break;  // a whole warp without items
       const bool real = i + mine < cnt;
       const int weight = describe_item(p, real ? g0 + i + mine : p.items);
       if (real && (tid & (p.lanes - 1)) == 0) s_weight[i + mine] = weight;
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const __grid_
     __syncthreads();
     if (tid < BLOCKS) {
       cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
-      *cluster.map_shared_rank(&s_block[rank], tid) = s_sum[kPlanThreads - 1];
+      *cluster.map_shared_rank(&s_block[rank], tid) = s_sum[THREADS - 1];
     }
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
@@ -346,18 +355,20 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const __grid_
     }
   } else {
     __syncthreads();
-    total = s_sum[kPlanThreads - 1];
+    total = s_sum[THREADS - 1];
   }
-  const long long stop = begin + s_sum[kPlanThreads - 1];
   const int n = (int)max(min((long long)p.warps, total / kRangeWeight), 1ll);
-  const long long each = total / n, more = total - each * n;
-  for (int k = tid; k <= p.warps; k += kPlanThreads) {
-    if (k >= n) {  // ends of the last range, and empty ones
-      if (rank == 0) p.range[k] = DecodeRange{p.items, 0};
-      continue;
-    }
+  const long long each = divide(total, n), more = total - each * n;
+  if (rank == 0)  // ends of the last range, and empty ones
+    for (int k = n + tid; k <= p.warps; k += THREADS) p.range[k] = DecodeRange{p.items, 0};
+  // range k begins at each k + min(k, more); the first that does so at or after x
+  auto first_from = [&](long long x) {
+    const long long wide = more * (each + 1);
+    return (int)(x <= wide ? divide(x + each, each + 1) : more + divide(x - wide + each - 1, each));
+  };
+  const int k1 = BLOCKS > 1 ? min(first_from(begin + s_sum[THREADS - 1]), n) : n;
+  for (int k = (BLOCKS > 1 ? first_from(begin) : 0) + tid; k < k1; k += THREADS) {
     const long long t0 = each * k + min((long long)k, more);
-    if (t0 < begin || t0 >= stop) continue;
     int a = 0, e = cnt - 1;  // first group whose inclusive sum is above t0
     while (a < e) {
       const int m = (a + e) >> 1;
@@ -608,28 +619,33 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   float acc[MT][NB][4];
   float m[2 * NB], mv[2 * NB], l[2 * NB], fac[2 * NB];  // of columns nb * 8 + 2 c + e
   uint32_t in_pat[2 * NB];   // patterns that each of the lane's heads takes part in
-  auto begin_item = [&](int item) {
+  uint2 raw[NB][MT];  // q of head nb * 8 + g mod HW
+  auto load_q = [&](int item) {
     const DecodeItem it = item_of(p, item);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int hl = nb * 8 + (g & (HW - 1));
+#pragma unroll
+      for (int k = 0; k < MT; ++k) {
+        const int d0 = (k >> 2) * 64 + c * 16 + (k & 3) * 4;
+        raw[nb][k] = hl < it.nh ? *reinterpret_cast<const uint2*>(p.q + (long long)it.token * p.q_stride +
+                                                                  (it.h0 + hl) * D + d0)
+                                : make_uint2(0, 0);
+      }
+    }
+  };
+  auto begin_item = [&](int item) {
     tiles = item == end.item ? end.tile : p.head[item].tiles;
     const uint32_t heads = lane < p.npat ? p.walk[(size_t)item * p.npat + lane].heads : 0u;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      // q of head nb * 8 + g mod HW, lifted by a power of two to [2^13, 2^14): exact in fp16
+      // q lifted by a power of two to [2^13, 2^14): exact in fp16
       // (elements under 2^-37 of the largest are cut)
-      const int hl = nb * 8 + (g & (HW - 1));
-      uint2 raw[MT];
       uint32_t big = 0;
 #pragma unroll
       for (int k = 0; k < MT; ++k) {
-        const int d0 = (k >> 2) * 64 + c * 16 + (k & 3) * 4;
-        raw[k] = hl < it.nh ? *reinterpret_cast<const uint2*>(p.q + (long long)it.token * p.q_stride +
-                                                              (it.h0 + hl) * D + d0)
-                            : make_uint2(0, 0);
-      }
-#pragma unroll
-      for (int k = 0; k < MT; ++k) {
-        big = max(max(big, raw[k].x & 0x7fffu), (raw[k].x >> 16) & 0x7fffu);
-        big = max(max(big, raw[k].y & 0x7fffu), (raw[k].y >> 16) & 0x7fffu);
+        big = max(max(big, raw[nb][k].x & 0x7fffu), (raw[nb][k].x >> 16) & 0x7fffu);
+        big = max(max(big, raw[nb][k].y & 0x7fffu), (raw[nb][k].y >> 16) & 0x7fffu);
       }
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -640,10 +656,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
       const float f1 = __uint_as_float((uint32_t)(u1 + 127) << 23), f2 = __uint_as_float((uint32_t)(u2 + 127) << 23);
 #pragma unroll
       for (int k = 0; k < MT; ++k) {
-        const __half2 a = __floats2half2_rn(__uint_as_float(raw[k].x << 16) * f1 * f2,
-                                            __uint_as_float(raw[k].x & 0xffff0000u) * f1 * f2);
-        const __half2 b = __floats2half2_rn(__uint_as_float(raw[k].y << 16) * f1 * f2,
-                                            __uint_as_float(raw[k].y & 0xffff0000u) * f1 * f2);
+        const __half2 a = __floats2half2_rn(__uint_as_float(raw[nb][k].x << 16) * f1 * f2,
+                                            __uint_as_float(raw[nb][k].x & 0xffff0000u) * f1 * f2);
+        const __half2 b = __floats2half2_rn(__uint_as_float(raw[nb][k].y << 16) * f1 * f2,
+                                            __uint_as_float(raw[nb][k].y & 0xffff0000u) * f1 * f2);
         qf[(nb * MT + k) * 32] = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
                                             *reinterpret_cast<const uint32_t*>(&b));
       }
@@ -719,6 +735,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   };
 
   // ---- start: the walk that the first tile belongs to
+  load_q(a_item);
   const DecodeWalk wk = load_walks(a_item);
   a_tiles -= rg.tile;
   if (rg.tile == 0) {
@@ -738,7 +755,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   look_up();
   int item = rg.item;
   bool from_start = rg.tile == 0;
-  begin_item(item);  // its loads go with the first tile's page numbers
+  begin_item(item);  // while the first tile's page numbers come
   tiles -= rg.tile;
   resolve();
   load_k();
@@ -916,7 +933,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
       end_item(item, !from_start ? 0 : item == end.item ? 1 : -1);
       if (more) {
         from_start = true;
-        begin_item(++item);
+        load_q(++item);
+        begin_item(item);
       }
     }
   }
@@ -961,8 +979,9 @@ __device__ __forceinline__ void store_joined(const DecodeParams& p, int D, size_
 }
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int LANES = D / 4;  // threads of a row
+__global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int LANES = D / 4, ROWS = 32 / LANES;  // threads of a row, rows that a warp reads at a time
+  constexpr int EAGER = 4;
   __shared__ float s_l[kJoinPart], s_v[kJoinPart];
   __shared__ float s_red[kJoinWarps][2];
   __shared__ float4 s_acc[kJoinThreads / LANES][LANES];
@@ -984,6 +1003,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
       r.item = __ldcg(reinterpret_cast<const int2*>(p.range + w_own + 1 + lane)).x;
   }
   grid_dependency_wait();
+  grid_dependency_release();
   __syncthreads();
   {
     const int w = w_own;
@@ -997,19 +1017,29 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
         const int n = __popc(held) + 1;
         const float* first = p.part + ((size_t)w * 2 + 1) * p.part_stride;
         const float* rest = p.part + (size_t)(w + 1) * 2 * p.part_stride - step;  // partial k at rest + k step
+        const int row = lane / LANES, col = lane % LANES;
         float4 st = make_float4(kNoMax, kNoMax, 0.f, 0.f);
         if (lane < n) st = *reinterpret_cast<const float4*>((lane == 0 ? first : rest + lane * step) + so);
+        float4 x[EAGER];  // the first rows come along with the statistics
+#pragma unroll
+        for (int i = 0; i < EAGER; ++i) {
+          const int k = i * ROWS + row;
+          if (k < n) x[i] = *reinterpret_cast<const float4*>((k == 0 ? first : rest + k * step) + hl * D + col * 4);
+        }
         const float M = warp_max(st.x), MV = warp_max(st.y);
         const float L = warp_sum(lane < n ? st.z * exp2f(st.x - M) : 0.f);
         const float f = exp2f(st.y - MV);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int row = lane / LANES, col = lane % LANES;
+#pragma unroll
+        for (int i = 0; i < EAGER; ++i) {
+          const float fk = __shfl_sync(0xffffffffu, f, i * ROWS + row);
+          if (i * ROWS + row < n) add_scaled(acc, x[i], fk);
+        }
 #pragma unroll 8
-        for (int k0 = 0; k0 < n; k0 += 32 / LANES) {
+        for (int k0 = EAGER * ROWS; k0 < n; k0 += ROWS) {
           const int k = k0 + row;
-          const float fk = __shfl_sync(0xffffffffu, f, k);
-          if (k < n)
-            add_scaled(acc, *reinterpret_cast<const float4*>((k == 0 ? first : rest + k * step) + hl * D + col * 4), fk);
+          const float fk = __shfl_sync(0xffffffffu, f, k & 31);
+          if (k < n) add_scaled(acc, *reinterpret_cast<const float4*>(rest + k * step + hl * D + col * 4), fk);
         }
         if constexpr (LANES == 16) {
           acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
@@ -1029,13 +1059,13 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   const float* first = p.part + ((size_t)w * 2 + 1) * p.part_stride;
   const float* rest = p.part + (size_t)(w + 1) * 2 * p.part_stride - step;
   // partials and their maxima
-  int n = 1;
-  float2 top = *reinterpret_cast<const float2*>(first + so);
-  for (int k = 1 + tid;; k += kJoinThreads) {
+  int n = 0;
+  float2 top = make_float2(kNoMax, kNoMax);
+  for (int k = tid;; k += kJoinThreads) {
     bool mine = w + k < p.warps;
-    if (mine) mine = p.range[w + k].item == item;
+    if (mine) mine = k == 0 || p.range[w + k].item == item;
     if (mine) {
-      const float2 f = *reinterpret_cast<const float2*>(rest + k * step + so);
+      const float2 f = *reinterpret_cast<const float2*>((k == 0 ? first : rest + k * step) + so);
       top.x = fmaxf(top.x, f.x);
       top.y = fmaxf(top.y, f.y);
     }

@@ -1171,7 +1171,7 @@ cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, s
 
 template <int D, int FMT>
 cudaError_t launch_cache_write(const CacheWriteParams& p, long long units, int page_size, cudaStream_t stream) {
-  if (p.tok.offsets == nullptr)
+  if (p.tok.offsets == nullptr || p.tok.T <= 8 * (long long)p.geom.B)
     return launch_overlapped(cache_append_kernel<D, FMT>, dim3((unsigned)((units + 7) / 8)), 256, 0, stream, p);
   // 64 numbers a lane
   const int warps = std::max(1, page_size * D / 2048);
@@ -1322,8 +1322,9 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   if (p.group > 1)
     e = launch_overlapped(decode_walks_kernel, dim3((unsigned)groups), kWalkThreads, 0, stream, p);
   if (e == cudaSuccess)
-    e = groups <= kPlanThreads / p.lanes && p.group == 1
-            ? launch_overlapped(decode_plan_kernel<1>, dim3(1), kPlanThreads, 0, stream, p)
+    // one block saves the cluster's barriers as long as it describes all items at once
+    e = groups <= kPlanAlone / p.lanes && p.group == 1
+            ? launch_overlapped(decode_plan_kernel<1>, dim3(1), kPlanAlone, 0, stream, p)
             : launch_overlapped<kPlanBlocks>(decode_plan_kernel<kPlanBlocks>, dim3(kPlanBlocks), kPlanThreads, 0,
                                              stream, p);
   if (e != cudaSuccess) return e;

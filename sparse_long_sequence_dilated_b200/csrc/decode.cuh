@@ -21,7 +21,8 @@
 // item that is cut leaves partials that decode_join_kernel combines in warp
 // order (no atomics: the same call gives the same bits).
 //
-// Launches: decode_plan_kernel, one block or cluster, describes every item's walks once
+// Launches: few short items have decode_cluster_kernel alone. Otherwise
+// decode_plan_kernel, one block or cluster, describes every item's walks once
 // and cuts the sequence (above kPlanBlocks * kPlanThreads items,
 // decode_walks_kernel describes them before it, over the whole GPU), then
 // decode_kernel, then decode_join_kernel. Each is launched while the one before
@@ -85,6 +86,7 @@ struct DecodeParams {
   int group;                 // items of a group: 1, or what a block of decode_walks_kernel describes
   int lanes;                 // threads that describe an item: a power of two, at least npat
   int warps;                 // warps of the grid
+  int clusters;              // a cluster for each item
   float qk_scale;            // log2(e) / sqrt(d)
   int npat;                  // patterns, by ascending r
   int dense;                 // one pattern with r = 1: every head takes every row of a walk
@@ -182,7 +184,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // Writes an item's head and walks; returns its weight. p.lanes threads
 // of a warp work on an item, lane j of them on pattern j; all 32 take part.
-__device__ int describe_item(const DecodeParams& p, int item) {
+__device__ int describe_item(const DecodeParams& p, int item, DecodeHead* head, DecodeWalk* walk) {
   const bool real = item < p.items;
   const DecodeItem it = item_of(p, real ? item : 0);
   const int j = threadIdx.x & (p.lanes - 1), jj = min(j, p.npat - 1);
@@ -227,7 +229,7 @@ __device__ int describe_item(const DecodeParams& p, int item) {
   }
   if (wk.n > 0 && limit <= hd.pos)
     wk.n = limit > wk.base ? (int)udiv((uint32_t)(limit - 1 - wk.base), r_mul, r_sh) + 1 : 0;
-  if (real && j < p.npat) p.walk[(size_t)item * p.npat + j] = wk;
+  if (real && j < p.npat) walk[j] = wk;
   int tiles = (int)(((uint32_t)wk.n + kDecTile - 1) / kDecTile);
   int weight = tiles * (r == 1 ? kTileWeight : kSpreadWeight);
   for (int d = 1; d < p.lanes; d <<= 1) {
@@ -236,7 +238,7 @@ __device__ int describe_item(const DecodeParams& p, int item) {
   }
   // an item without rows keeps one empty tile: the warp that has it writes its zeros
   hd.tiles = max(tiles, 1);
-  if (real && j == 0) p.head[item] = hd;
+  if (real && j == 0) *head = hd;
   return kItemWeight + max(weight, kTileWeight);
 }
 
@@ -286,7 +288,8 @@ __global__ void __launch_bounds__(kWalkThreads)
   const int end = (int)min(first + p.group, (long long)p.items);
   long long run = 0;
   for (int i = (int)first; i < end; i += per) {
-    const int weight = describe_item(p, i + mine);
+    const int item_l = i + mine;
+    const int weight = describe_item(p, item_l, p.head + item_l, p.walk + (size_t)item_l * p.npat);
     if ((threadIdx.x & (p.lanes - 1)) == 0) s_weight[mine] = weight;
     __syncthreads();
     const int item = i + threadIdx.x;
@@ -329,7 +332,8 @@ __global__ void __launch_bounds__(BLOCKS > 1 ? kPlanThreads : kPlanAlone)
     for (int i = 0; i < cnt; i += at_once) {
       if (i + (tid & ~31) / p.lanes >= cnt) break;  // a whole warp without items
       const bool real = i + mine < cnt;
-      const int weight = describe_item(p, real ? g0 + i + mine : p.items);
+      const int item = real ? g0 + i + mine : p.items;
+      const int weight = describe_item(p, item, p.head + item, p.walk + (size_t)item * p.npat);
       if (real && (tid & (p.lanes - 1)) == 0) s_weight[i + mine] = weight;
     }
     __syncthreads();
@@ -450,30 +454,24 @@ __device__ __forceinline__ float final_lse(float m, float l) {
 // the softmax sum uses p = 2^(s - m) in fp32. p' is rounded to fp16 for the
 // product (2^-11 relative, below the bf16 rounding of the result).
 // ---------------------------------------------------------------------------
+
+// One warp's tiles from rg up to end. Items' heads and walks are at head[0] and
+// walk[0] from item first_item on; part: the warp's two slots for partials, slot_stride
+// floats apart; qf, s_walk: shared memory of the warp (the lane's own fragments
+// of Q, NB * MT of them 32 apart, and the walks of the item to fetch from).
 template <int D, int HEADS, int FMT>
-__global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>::BLOCKS_PER_SM))
-    decode_kernel(const __grid_constant__ DecodeParams p) {
+__device__ __forceinline__ void decode_range(const DecodeParams& p, const DecodeRange rg, const DecodeRange end,
+                                             const DecodeHead* head, const DecodeWalk* walk, int first_item,
+                                             float* part, size_t slot_stride, uint2* qf, DecodeWalk* s_walk) {
   constexpr int NB = (HEADS + 7) / 8;
   constexpr int MT = D / 16;                       // M tiles of O^T; k-steps of S
   constexpr int HW = HEADS < 8 ? HEADS : 8;        // heads of an MMA's columns
   constexpr int VR = HW <= 2 ? 1 : HW / 2;         // rows of a tile that a lane's softmax has
   constexpr int VE = HW == 1 ? 1 : 2;              // heads of them, for each NB
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int row_l = 8 * c + g;                     // the row this lane looks up
   const int first_slot = VR == 1 ? c : VR == 2 ? (c & 2) : 0;
-  // the lane's own fragments of Q, where registers are short
-  __shared__ uint2 s_q[kDecWarps][NB * MT * 32];
-  uint2* const qf = s_q[warp] + lane;
-  __shared__ DecodeWalk s_walk[kDecWarps][kMaxPat];  // of the item to fetch from
-  // neighbouring warps of the sequence on different SMs: few ranges spread over all
-  const int wi = warp * (int)gridDim.x + (int)blockIdx.x;
-
-  grid_dependency_wait();
-  const DecodeRange rg = p.range[wi], end = p.range[wi + 1];
-  grid_dependency_release();
-  if (rg.item == end.item && rg.tile == end.tile) return;
-
   const int pmask = (1 << p.geom.lp) - 1;
 
   // ---- the walk to fetch from (a_...), the looked-up tile (f_...), the tile in registers
@@ -484,7 +482,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   bool a_some = true, f_some = false, f_whole = false;
 
   auto set_walk = [&](int j) {
-    const DecodeWalk wk = s_walk[warp][j];
+    const DecodeWalk wk = s_walk[j];
     a_j = j;
     a_n = wk.n;
     a_base = wk.base;
@@ -492,15 +490,15 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   };
   auto load_walks = [&](int item) {  // returns this lane's
     DecodeWalk wk{0x7fffffff, 0, 0, 0u};
-    if (lane < p.npat) wk = p.walk[(size_t)item * p.npat + lane];
-    const DecodeHead hd = p.head[item];
+    if (lane < p.npat) wk = walk[(size_t)(item - first_item) * p.npat + lane];
+    const DecodeHead hd = head[item - first_item];
     a_pos = hd.pos;
     a_b = hd.b;
     a_hk = item_of(p, item).hk;
     a_tiles = item == end.item ? end.tile : hd.tiles;
     a_walks = __ballot_sync(0xffffffffu, wk.n > 0);
     a_in = __ballot_sync(0xffffffffu, wk.heads & 1u);
-    if (lane < kMaxPat) s_walk[warp][lane] = wk;
+    if (lane < kMaxPat) s_walk[lane] = wk;
     __syncwarp();
     return wk;
   };
@@ -529,7 +527,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
       const int last = (int)((uint32_t)a_base + min(a_k + kDecTile - 1, n - 1) * (uint32_t)a_r);
       uint32_t held = 1u << a_j;
       for (int i = 0; i < p.npat; ++i) {
-        const int si = s_walk[warp][i].s;
+        const int si = s_walk[i].s;
         if (i == a_j || last < si) continue;
         if (f_x >= si && divides(p, i, a_pos - f_x)) held |= 1u << i;
       }
@@ -635,8 +633,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
     }
   };
   auto begin_item = [&](int item) {
-    tiles = item == end.item ? end.tile : p.head[item].tiles;
-    const uint32_t heads = lane < p.npat ? p.walk[(size_t)item * p.npat + lane].heads : 0u;
+    tiles = item == end.item ? end.tile : head[item - first_item].tiles;
+    const uint32_t heads = lane < p.npat ? walk[(size_t)(item - first_item) * p.npat + lane].heads : 0u;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       // q lifted by a power of two to [2^13, 2^14): exact in fp16
@@ -693,7 +691,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   // The item is done here (slot < 0: this warp had all of it), or a partial of it goes to the slot.
   auto end_item = [&](int item, int slot) {
     const DecodeItem it = item_of(p, item);
-    float* const dst = p.part + ((size_t)wi * 2 + max(slot, 0)) * p.part_stride;
+    float* const dst = part + max(slot, 0) * slot_stride;
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i) {
 #pragma unroll
@@ -729,7 +727,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
                 make_float4(sum_of(nb, e, 4 * k), sum_of(nb, e, 4 * k + 1), sum_of(nb, e, 4 * k + 2),
                             sum_of(nb, e, 4 * k + 3));
           if (g == 0)
-            *reinterpret_cast<float4*>(dst + p.part_heads * D + hl * 4) = make_float4(m[i], mv[i], l[i], 0.f);
+            *reinterpret_cast<float4*>(dst + p.part_heads * D + hl * 4) = make_float4(m[i], mv[i], l[i], 1.f);
         }
       }
   };
@@ -940,16 +938,21 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   }
 }
 
-// ---------------------------------------------------------------------------
-// Join of cut items. An item that begins in warp w's range and goes on past it
-// has its partials in slot 1 of w and in slot 0 of the warps behind it. A block
-// has the items that begin in kJoinWarps successive ranges, and one head of
-// them. An item of up to 32 partials is one warp's; longer ones (at most one
-// begins within so few ranges) are the whole block's.
-// ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 8;
-constexpr int kJoinThreads = kJoinWarps * 32;
-constexpr int kJoinPart = 512;  // partials whose weights are held at a time
+template <int D, int HEADS, int FMT>
+__global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>::BLOCKS_PER_SM))
+    decode_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ uint2 s_q[kDecWarps][(HEADS + 7) / 8 * D / 16 * 32];
+  __shared__ DecodeWalk s_walk[kDecWarps][kMaxPat];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // neighbouring warps of the sequence on different SMs: few ranges spread over all
+  const int wi = warp * (int)gridDim.x + (int)blockIdx.x;
+  grid_dependency_wait();
+  const DecodeRange rg = p.range[wi], end = p.range[wi + 1];
+  grid_dependency_release();
+  if (rg.item == end.item && rg.tile == end.tile) return;
+  decode_range<D, HEADS, FMT>(p, rg, end, p.head, p.walk, 0, p.part + (size_t)wi * 2 * p.part_stride, p.part_stride,
+                              s_q[warp] + lane, s_walk[warp]);
+}
 
 __device__ __forceinline__ void add_scaled(float4& a, const float4& x, float f) {
   a.x += x.x * f;
@@ -977,6 +980,94 @@ __device__ __forceinline__ void store_joined(const DecodeParams& p, int D, size_
       make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   if (col == 0 && p.lse != nullptr) p.lse[oi] = final_lse(M, L);
 }
+
+// ---------------------------------------------------------------------------
+// Few short items: a cluster for each, in one launch. Every block describes the
+// item, its warps take equal shares of the tiles, and the partials come
+// together in shared memory, the block's first and then the cluster's.
+// ---------------------------------------------------------------------------
+constexpr int kClusterBlocks = 8;
+constexpr int kClusterWarps = 8;
+constexpr int kClusterTiles = 8 * kClusterBlocks * kClusterWarps;  // most tiles of an item
+
+template <int D, int HEADS, int FMT>
+__global__ void __launch_bounds__(kClusterWarps * 32, D == 64 ? 2 : 1)
+    decode_cluster_kernel(const __grid_constant__ DecodeParams p) {
+  static_assert(HEADS <= 8, "the partials of more take too much shared memory");
+  extern __shared__ float4 s_dyn[];       // partials of the warps, then the block's
+  __shared__ uint2 s_q[kClusterWarps][D / 16 * 32];
+  __shared__ DecodeWalk s_walk[kClusterWarps][kMaxPat];
+  __shared__ DecodeWalk s_desc[kMaxPat];
+  __shared__ DecodeHead s_head;
+  float* const s_part = reinterpret_cast<float*>(s_dyn);
+  float* const s_block = s_part + kClusterWarps * p.part_stride;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int item = (int)blockIdx.x / kClusterBlocks, rank = (int)blockIdx.x % kClusterBlocks;
+  const int stat = p.part_heads * D;      // where a partial's statistics begin
+  grid_dependency_wait();
+  grid_dependency_release();
+  if (warp == 0) describe_item(p, item, &s_head, s_desc);
+  __syncthreads();
+  {
+    const int k = warp * kClusterBlocks + rank;
+    const DecodeRange rg{item, s_head.tiles * k / (kClusterBlocks * kClusterWarps)};
+    const DecodeRange end{item, s_head.tiles * (k + 1) / (kClusterBlocks * kClusterWarps)};
+    float* const part = s_part + warp * p.part_stride;
+    if (rg.tile < end.tile)
+      decode_range<D, HEADS, FMT>(p, rg, end, &s_head, s_desc, item, part, 0, s_q[warp] + lane, s_walk[warp]);
+    else if (lane < p.part_heads)
+      reinterpret_cast<float4*>(part + stat)[lane] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+  }
+  __syncthreads();
+  const DecodeItem it = item_of(p, item);
+  const int pieces = it.nh * (D / 4);
+  // element piece i of `n` partials, the k-th one at part(k); those whose mark is 0 are not there
+  auto join = [&](auto part, int n, int i, float& M, float& MV, float& L) {
+    const int hl = i / (D / 4);
+    M = MV = kNoMax;
+    L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < n; ++k) {
+      const float4 st = *reinterpret_cast<const float4*>(part(k) + stat + hl * 4);
+      M = fmaxf(M, st.x);
+      MV = fmaxf(MV, st.y);
+    }
+    for (int k = 0; k < n; ++k) {
+      const float4 st = *reinterpret_cast<const float4*>(part(k) + stat + hl * 4);
+      if (st.w == 0.f) continue;
+      L += st.z * exp2f(st.x - M);
+      add_scaled(a, reinterpret_cast<const float4*>(part(k))[i], exp2f(st.y - MV));
+    }
+    return a;
+  };
+  for (int i = tid; i < pieces; i += kClusterWarps * 32) {
+    float M, MV, L;
+    reinterpret_cast<float4*>(s_block)[i] =
+        join([&](int k) { return s_part + k * p.part_stride; }, kClusterWarps, i, M, MV, L);
+    if (i % (D / 4) == 0) *reinterpret_cast<float4*>(s_block + stat + i / (D / 4) * 4) = make_float4(M, MV, L, 1.f);
+  }
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  cluster.sync();
+  for (int i = tid * kClusterBlocks + rank; i < pieces; i += kClusterWarps * 32 * kClusterBlocks) {
+    float M, MV, L;
+    const float4 a = join([&](int k) { return (const float*)cluster.map_shared_rank(s_block, k); }, kClusterBlocks, i,
+                          M, MV, L);
+    const int hl = i / (D / 4);
+    store_joined(p, D, (size_t)it.token * p.H + it.h0 + hl, i % (D / 4), a, M, MV, L);
+  }
+  cluster.sync();  // no block ends while another reads its sums
+}
+
+// ---------------------------------------------------------------------------
+// Join of cut items. An item that begins in warp w's range and goes on past it
+// has its partials in slot 1 of w and in slot 0 of the warps behind it. A block
+// has the items that begin in kJoinWarps successive ranges, and one head of
+// them. An item of up to 32 partials is one warp's; longer ones (at most one
+// begins within so few ranges) are the whole block's.
+// ---------------------------------------------------------------------------
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinPart = 512;  // partials whose weights are held at a time
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __grid_constant__ DecodeParams p) {

@@ -1315,8 +1315,23 @@ DecodeScratch decode_scratch(int T, int H, int Hkv, int d) {
   return s;
 }
 
+size_t cluster_smem(const DecodeParams& p) { return (size_t)(kClusterWarps + 1) * p.part_stride * 4; }
+
 template <int D, int HEADS, int FMT>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
+  if constexpr (HEADS <= 8) {
+    if (p.clusters) {
+      // more than 48 KB with the static part; opting in is needed once per device and costs nothing to repeat
+      if constexpr (D == 128 && HEADS == 8) {
+        const cudaError_t e = cudaFuncSetAttribute(decode_cluster_kernel<D, HEADS, FMT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cluster_smem(p));
+        if (e != cudaSuccess) return e;
+      }
+      return launch_overlapped<kClusterBlocks>(decode_cluster_kernel<D, HEADS, FMT>,
+                                               dim3((unsigned)(p.items * kClusterBlocks)), kClusterWarps * 32,
+                                               cluster_smem(p), stream, p);
+    }
+  }
   const int groups = (int)(((long long)p.items + p.group - 1) / p.group);
   cudaError_t e = cudaSuccess;
   if (p.group > 1)
@@ -1470,6 +1485,9 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   double rows = 0;
   for (int i = 0; i < npat; ++i) rows += (double)std::min<long long>(w[i], longest) / r[i] + 1;
   const double tiles = (rows / kDecTile + npat) * p.items;
+  // a cluster for each item: as many items as surely run at once (two clusters in each of eight
+  // groups of SMs, at d = 64 twice that), none of more than eight tiles a warp
+  p.clusters = p.G <= 8 && p.items <= (d == 64 ? 32 : 16) && rows / kDecTile + npat <= kClusterTiles;
   const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(p.G, d);
   p.warps = kDecWarps * (int)std::min<double>(blocks, tiles * kSpreadWeight / (kDecWarps * kRangeWeight) + 1);
   cudaError_t e;

@@ -28,6 +28,29 @@ def run(pair, table, q, pos, pats, seq=None, **kw):
     return got, ref.decode(q, pair.ref, table, pos, seq, pats)
 
 
+@pytest.mark.parametrize("copies", [1, 7])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (4, 2), (4, 1), (7, 1), (13, 1)])
+@pytest.mark.parametrize("pats", sorted(PATS))
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_tokens_and_many(copies, H, Hkv, pats, fmt, d):
+    """The same tokens few at a time (a cluster for each token and KV head) and seven times over
+    (ranges of the whole call's tiles): every copy has the token's result."""
+    rng = np.random.default_rng(d + H)
+    lens = [1, 40, 333, 1900]
+    pair, table = filled(rng, lens, Hkv, 16, d, fmt, spread=3)
+    pos, seq = [0, 39, 332, 1899, 1030, -1], [0, 1, 2, 3, 3, 0]
+    q = normal(rng, len(pos), H, d)
+    want = ref.decode(q, pair.ref, table, pos, seq, PATS[pats])
+    out, lse = dilattn.decode(bf16(np.tile(q, (copies, 1, 1))).cuda(), pair.dev, i32(table), i32(pos * copies),
+                              PATS[pats], seq=i32(seq * copies))
+    torch.cuda.synchronize()
+    assert dilattn.device_error() == 0
+    n = len(pos)
+    for k in range(copies):
+        check_decode((out[k * n:(k + 1) * n], lse[k * n:(k + 1) * n]), want, q, pair)
+
+
 @pytest.mark.parametrize("pats", sorted(PATS))
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("d", [64, 128])

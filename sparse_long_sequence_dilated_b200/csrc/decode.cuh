@@ -21,7 +21,7 @@
 // item that is cut leaves partials that decode_join_kernel combines in warp
 // order (no atomics: the same call gives the same bits).
 //
-// Launches: few short items have decode_cluster_kernel alone. Otherwise
+// Launches: few or short items have decode_team_kernel alone. Otherwise
 // decode_plan_kernel, one block or cluster, describes every item's walks once
 // and cuts the sequence (above kPlanBlocks * kPlanThreads items,
 // decode_walks_kernel describes them before it, over the whole GPU), then
@@ -86,7 +86,8 @@ struct DecodeParams {
   int group;                 // items of a group: 1, or what a block of decode_walks_kernel describes
   int lanes;                 // threads that describe an item: a power of two, at least npat
   int warps;                 // warps of the grid
-  int clusters;              // a cluster for each item
+  int team;                  // blocks that share an item in decode_team_kernel; 0: a warp for each item
+  int join_items;            // decode_join_kernel has a block for each item, not for every 8 ranges
   float qk_scale;            // log2(e) / sqrt(d)
   int npat;                  // patterns, by ascending r
   int dense;                 // one pattern with r = 1: every head takes every row of a walk
@@ -118,7 +119,8 @@ template <int D_, int NB_>
 struct DecodeCfg {
   static constexpr int D = D_, NB = NB_;
   static constexpr int HEADS = 8 * NB;
-  static constexpr int BLOCKS_PER_SM = (D == 64 ? 4 : 3) - (NB - 1);  // by registers: 128, 168 or 255 a thread
+  // by registers: 128, 168 or 255 a thread; what does not fit would be loads under way
+  static constexpr int BLOCKS_PER_SM = NB == 2 ? 2 : D == 64 ? 4 : 3;
 };
 
 // Where an item belongs.
@@ -982,42 +984,49 @@ __device__ __forceinline__ void store_joined(const DecodeParams& p, int D, size_
 }
 
 // ---------------------------------------------------------------------------
-// Few short items: a cluster for each, in one launch. Every block describes the
-// item, its warps take equal shares of the tiles, and the partials come
-// together in shared memory, the block's first and then the cluster's.
+// Few or short items, in one launch. A team has an item: a warp (p.team = 0), or
+// the 8 warps each of p.team blocks of a cluster. It describes the item, its
+// warps take equal shares of the tiles, and the partials come together in
+// shared memory, the block's first and then the cluster's.
 // ---------------------------------------------------------------------------
-constexpr int kClusterBlocks = 8;
-constexpr int kClusterWarps = 8;
-constexpr int kClusterTiles = 8 * kClusterBlocks * kClusterWarps;  // most tiles of an item
+constexpr int kTeamBlocks = 8;        // most blocks of a team
+constexpr int kTeamWarps = 8;         // warps of a block
 
 template <int D, int HEADS, int FMT>
-__global__ void __launch_bounds__(kClusterWarps * 32, D == 64 ? 2 : 1)
-    decode_cluster_kernel(const __grid_constant__ DecodeParams p) {
-  static_assert(HEADS <= 8, "the partials of more take too much shared memory");
+__global__ void __launch_bounds__(kTeamWarps * 32, D == 64 && HEADS <= 8 ? 2 : 1)
+    decode_team_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ float4 s_dyn[];       // partials of the warps, then the block's
-  __shared__ uint2 s_q[kClusterWarps][D / 16 * 32];
-  __shared__ DecodeWalk s_walk[kClusterWarps][kMaxPat];
-  __shared__ DecodeWalk s_desc[kMaxPat];
-  __shared__ DecodeHead s_head;
+  __shared__ uint2 s_q[kTeamWarps][(HEADS + 7) / 8 * D / 16 * 32];
+  __shared__ DecodeWalk s_walk[kTeamWarps][kMaxPat], s_desc[kTeamWarps][kMaxPat];
+  __shared__ DecodeHead s_head[kTeamWarps];
   float* const s_part = reinterpret_cast<float*>(s_dyn);
-  float* const s_block = s_part + kClusterWarps * p.part_stride;
+  float* const s_block = s_part + kTeamWarps * p.part_stride;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int item = (int)blockIdx.x / kClusterBlocks, rank = (int)blockIdx.x % kClusterBlocks;
   const int stat = p.part_heads * D;      // where a partial's statistics begin
+  const bool alone = p.team == 0;
+  const int blocks = max(p.team, 1), rank = (int)blockIdx.x % blocks;
+  const int item = alone ? (int)blockIdx.x * kTeamWarps + warp : (int)blockIdx.x / blocks;
+  const int own = alone ? warp : 0;       // whose description it is
   grid_dependency_wait();
   grid_dependency_release();
-  if (warp == 0) describe_item(p, item, &s_head, s_desc);
-  __syncthreads();
+  if (alone && item >= p.items) return;
+  if (alone || warp == 0) describe_item(p, item, &s_head[own], s_desc[own]);
+  if (alone) __syncwarp(); else __syncthreads();
   {
-    const int k = warp * kClusterBlocks + rank;
-    const DecodeRange rg{item, s_head.tiles * k / (kClusterBlocks * kClusterWarps)};
-    const DecodeRange end{item, s_head.tiles * (k + 1) / (kClusterBlocks * kClusterWarps)};
+    DecodeRange rg{item, 0}, end{item + 1, 0};
+    if (!alone) {
+      const int k = warp * blocks + rank, n = blocks * kTeamWarps;
+      const long long tiles = s_head[0].tiles;
+      rg.tile = (int)(tiles * k / n);
+      end = DecodeRange{item, (int)(tiles * (k + 1) / n)};
+    }
     float* const part = s_part + warp * p.part_stride;
-    if (rg.tile < end.tile)
-      decode_range<D, HEADS, FMT>(p, rg, end, &s_head, s_desc, item, part, 0, s_q[warp] + lane, s_walk[warp]);
+    if (alone || rg.tile < end.tile)
+      decode_range<D, HEADS, FMT>(p, rg, end, &s_head[own], s_desc[own], item, part, 0, s_q[warp] + lane, s_walk[warp]);
     else if (lane < p.part_heads)
       reinterpret_cast<float4*>(part + stat)[lane] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
   }
+  if (alone) return;
   __syncthreads();
   const DecodeItem it = item_of(p, item);
   const int pieces = it.nh * (D / 4);
@@ -1040,17 +1049,17 @@ __global__ void __launch_bounds__(kClusterWarps * 32, D == 64 ? 2 : 1)
     }
     return a;
   };
-  for (int i = tid; i < pieces; i += kClusterWarps * 32) {
+  for (int i = tid; i < pieces; i += kTeamWarps * 32) {
     float M, MV, L;
     reinterpret_cast<float4*>(s_block)[i] =
-        join([&](int k) { return s_part + k * p.part_stride; }, kClusterWarps, i, M, MV, L);
+        join([&](int k) { return s_part + k * p.part_stride; }, kTeamWarps, i, M, MV, L);
     if (i % (D / 4) == 0) *reinterpret_cast<float4*>(s_block + stat + i / (D / 4) * 4) = make_float4(M, MV, L, 1.f);
   }
   cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
   cluster.sync();
-  for (int i = tid * kClusterBlocks + rank; i < pieces; i += kClusterWarps * 32 * kClusterBlocks) {
+  for (int i = tid * blocks + rank; i < pieces; i += kTeamWarps * 32 * blocks) {
     float M, MV, L;
-    const float4 a = join([&](int k) { return (const float*)cluster.map_shared_rank(s_block, k); }, kClusterBlocks, i,
+    const float4 a = join([&](int k) { return (const float*)cluster.map_shared_rank(s_block, k); }, blocks, i,
                           M, MV, L);
     const int hl = i / (D / 4);
     store_joined(p, D, (size_t)it.token * p.H + it.h0 + hl, i % (D / 4), a, M, MV, L);
@@ -1063,7 +1072,8 @@ __global__ void __launch_bounds__(kClusterWarps * 32, D == 64 ? 2 : 1)
 // has its partials in slot 1 of w and in slot 0 of the warps behind it. A block
 // has the items that begin in kJoinWarps successive ranges, and one head of
 // them. An item of up to 32 partials is one warp's; longer ones (at most one
-// begins within so few ranges) are the whole block's.
+// begins within so few ranges) are the whole block's. Fewer items than there
+// would be blocks have a block each (p.join_items).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
@@ -1078,26 +1088,49 @@ __global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __gr
   __shared__ float4 s_acc[kJoinThreads / LANES][LANES];
   __shared__ int s_long;        // range in which an item of more than 32 partials begins
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hl = blockIdx.y;
-  const int w0 = blockIdx.x * kJoinWarps;
   const size_t step = (size_t)2 * p.part_stride;
   const int so = p.part_heads * D + hl * 4;
-  if (tid == 0) s_long = -1;
+  int w = -1, n = 0;            // range in which the block's item begins, and its partials
   // The ranges are there: this kernel was let start after every block of the main one had waited
   // for the plan. What other kernels left of them in L1 is passed over.
-  const int w_own = w0 + warp;
-  DecodeRange a{0, 0}, b{0, 0}, r{-1, 0};  // r: ranges w_own + 1 .., those that hold a part of the item
-  if (w_own < p.warps) {
-    const int2 x = __ldcg(reinterpret_cast<const int2*>(p.range + w_own));
-    const int2 y = __ldcg(reinterpret_cast<const int2*>(p.range + w_own + 1));
-    a = DecodeRange{x.x, x.y}, b = DecodeRange{y.x, y.y};
-    if (w_own + 1 + lane < p.warps)
-      r.item = __ldcg(reinterpret_cast<const int2*>(p.range + w_own + 1 + lane)).x;
-  }
-  grid_dependency_wait();
-  grid_dependency_release();
-  __syncthreads();
-  {
-    const int w = w_own;
+  auto range = [&](int k) {
+    const int2 x = __ldcg(reinterpret_cast<const int2*>(p.range + k));
+    return DecodeRange{x.x, x.y};
+  };
+  if (p.join_items) {
+    const int item = (int)blockIdx.x;
+    int before = 0, in = 0;     // ranges that begin up to the item's beginning, and inside it
+    for (int k = tid; k <= p.warps; k += kJoinThreads) {
+      const DecodeRange r = range(k);
+      before += r.item < item || (r.item == item && r.tile == 0);
+      in += r.item == item && r.tile > 0;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    in = __reduce_add_sync(0xffffffffu, in);
+    if (lane == 0) s_red[warp][0] = __int_as_float(before), s_red[warp][1] = __int_as_float(in);
+    __syncthreads();
+    before = in = 0;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) before += __float_as_int(s_red[k][0]), in += __float_as_int(s_red[k][1]);
+    __syncthreads();
+    grid_dependency_wait();
+    grid_dependency_release();
+    if (in == 0) return;
+    w = before - 1;
+    n = in + 1;
+  } else {
+    if (tid == 0) s_long = -1;
+    const int w_own = (int)blockIdx.x * kJoinWarps + warp;
+    DecodeRange a{0, 0}, b{0, 0}, r{-1, 0};  // r: ranges w_own + 1 .., those that hold a part of the item
+    if (w_own < p.warps) {
+      a = range(w_own);
+      b = range(w_own + 1);
+      if (w_own + 1 + lane < p.warps) r = range(w_own + 1 + lane);
+    }
+    grid_dependency_wait();
+    grid_dependency_release();
+    __syncthreads();
+    w = w_own;
     const DecodeItem it = item_of(p, b.tile > 0 ? b.item : 0);
     // an item begins in range w and goes on past it
     if (b.tile > 0 && (a.item != b.item || a.tile == 0) && hl < it.nh) {
@@ -1141,28 +1174,27 @@ __global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __gr
         if (row == 0) store_joined(p, D, (size_t)it.token * p.H + it.h0 + hl, col, acc, M, MV, L);
       }
     }
+    __syncthreads();
+    w = s_long;
+    if (w < 0) return;
+    const int item = range(w + 1).item;
+    for (int k = w + 1 + tid;; k += kJoinThreads) {
+      const int got = __syncthreads_count(k < p.warps && range(k).item == item);
+      n += got;
+      if (got < kJoinThreads) break;
+    }
+    ++n;
   }
-  __syncthreads();
-  const int w = s_long;
-  if (w < 0) return;
-  const int item = p.range[w + 1].item;
-  const DecodeItem it = item_of(p, item);
+  const DecodeItem it = item_of(p, p.join_items ? (int)blockIdx.x : range(w + 1).item);
+  if (hl >= it.nh) return;
   const float* first = p.part + ((size_t)w * 2 + 1) * p.part_stride;
   const float* rest = p.part + (size_t)(w + 1) * 2 * p.part_stride - step;
-  // partials and their maxima
-  int n = 0;
+  // the largest maxima
   float2 top = make_float2(kNoMax, kNoMax);
-  for (int k = tid;; k += kJoinThreads) {
-    bool mine = w + k < p.warps;
-    if (mine) mine = k == 0 || p.range[w + k].item == item;
-    if (mine) {
-      const float2 f = *reinterpret_cast<const float2*>((k == 0 ? first : rest + k * step) + so);
-      top.x = fmaxf(top.x, f.x);
-      top.y = fmaxf(top.y, f.y);
-    }
-    const int got = __syncthreads_count(mine);
-    n += got;
-    if (got < kJoinThreads) break;
+  for (int k = tid; k < n; k += kJoinThreads) {
+    const float2 f = *reinterpret_cast<const float2*>((k == 0 ? first : rest + k * step) + so);
+    top.x = fmaxf(top.x, f.x);
+    top.y = fmaxf(top.y, f.y);
   }
   float M = warp_max(top.x), MV = warp_max(top.y);
   if (lane == 0) s_red[warp][0] = M, s_red[warp][1] = MV;

@@ -1148,15 +1148,15 @@ int check_tokens(const void* k, const void* v, long long k_stride, long long v_s
 
 // A launch that may start while the kernel before it on the stream still
 // runs; the kernel itself waits for that one's end before it reads its results.
-template <int CLUSTER = 1, typename... Args>
+template <typename... Args>
 cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
-                              cudaStream_t stream, Args... args) {
+                              cudaStream_t stream, int cluster, Args... args) {
   cudaLaunchAttribute attr[2];
   memset(attr, 0, sizeof(attr));
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CLUSTER;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
@@ -1165,14 +1165,14 @@ cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, s
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int D, int FMT>
 cudaError_t launch_cache_write(const CacheWriteParams& p, long long units, int page_size, cudaStream_t stream) {
   if (p.tok.offsets == nullptr || p.tok.T <= 8 * (long long)p.geom.B)
-    return launch_overlapped(cache_append_kernel<D, FMT>, dim3((unsigned)((units + 7) / 8)), 256, 0, stream, p);
+    return launch_overlapped(cache_append_kernel<D, FMT>, dim3((unsigned)((units + 7) / 8)), 256, 0, stream, 1, p);
   // 64 numbers a lane
   const int warps = std::max(1, page_size * D / 2048);
   const dim3 grid((unsigned)((units * warps + 7) / 8));
@@ -1180,7 +1180,7 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, long long units, int p
                       : warps == 2 ? cache_write_kernel<D, FMT, 2>
                       : warps == 4 ? cache_write_kernel<D, FMT, 4>
                                    : cache_write_kernel<D, FMT, D / 16>;
-  return launch_overlapped(kernel, grid, 256, 0, stream, p);
+  return launch_overlapped(kernel, grid, 256, 0, stream, 1, p);
 }
 
 // Whether a written buffer overlaps a read one.
@@ -1280,7 +1280,7 @@ extern "C" int dilattn_cache_read(const void* kc, const void* vc, const float* k
   const auto kernel = format == DILATTN_CACHE_E4M3
                           ? (d == 64 ? cache_read_kernel<64, kFmtE4M3> : cache_read_kernel<128, kFmtE4M3>)
                           : (d == 64 ? cache_read_kernel<64, kFmtInt8> : cache_read_kernel<128, kFmtInt8>);
-  const cudaError_t e = launch_overlapped(kernel, grid, 256, 0, stream, p);
+  const cudaError_t e = launch_overlapped(kernel, grid, 256, 0, stream, 1, p);
   if (e != cudaSuccess) return cuda_fail(e, "cache_read_kernel launch");
   return DILATTN_OK;
 }
@@ -1294,7 +1294,20 @@ long long decode_items(int T, int Hkv, int G) {
   const int heads = decode_heads(G);
   return (long long)T * Hkv * ((G + heads - 1) / heads);
 }
-int decode_blocks_per_sm(int G, int d) { return (d == 64 ? 4 : 3) - (G > 8 ? 1 : 0); }
+int decode_blocks_per_sm(int G, int d) { return G > 8 ? 2 : d == 64 ? 4 : 3; }
+
+// Blocks of a team for `items` items of up to `tiles` tiles (see decode_team_kernel), or -1: they
+// are too many or too long, and ranges of all items' tiles serve better. A warp does up to eight
+// tiles in the time that the plan and the join would take; teams of blocks all run at once, in
+// eight groups of 16 or more SMs with one block on each (two at d = 64 and up to 8 heads), and
+// the larger the sooner they are done.
+int decode_team(int items, double tiles, int d, int heads) {
+  if (tiles <= 8) return 0;
+  const int each = d == 64 && heads <= 8 ? 2 : 1;
+  for (int team = kTeamBlocks; team >= 1; team /= 2)
+    if (tiles <= 8 * kTeamWarps * team && (double)items * team <= 128 * each) return team;
+  return -1;
+}
 
 // Workspace of a decode: the items' walks, the warps' ranges, and the partials of cut items.
 struct DecodeScratch {
@@ -1315,39 +1328,36 @@ DecodeScratch decode_scratch(int T, int H, int Hkv, int d) {
   return s;
 }
 
-size_t cluster_smem(const DecodeParams& p) { return (size_t)(kClusterWarps + 1) * p.part_stride * 4; }
-
 template <int D, int HEADS, int FMT>
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
-  if constexpr (HEADS <= 8) {
-    if (p.clusters) {
-      // more than 48 KB with the static part; opting in is needed once per device and costs nothing to repeat
-      if constexpr (D == 128 && HEADS == 8) {
-        const cudaError_t e = cudaFuncSetAttribute(decode_cluster_kernel<D, HEADS, FMT>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cluster_smem(p));
-        if (e != cudaSuccess) return e;
-      }
-      return launch_overlapped<kClusterBlocks>(decode_cluster_kernel<D, HEADS, FMT>,
-                                               dim3((unsigned)(p.items * kClusterBlocks)), kClusterWarps * 32,
-                                               cluster_smem(p), stream, p);
+  if (p.team >= 0) {
+    const auto kernel = decode_team_kernel<D, HEADS, FMT>;
+    const size_t smem = p.team == 0 ? 0 : (size_t)(kTeamWarps + 1) * p.part_stride * 4;
+    // with the static part more than 48 KB; opting in is needed once per device and costs nothing to repeat
+    if constexpr (HEADS * D >= 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
     }
+    const dim3 grid((unsigned)(p.team == 0 ? (p.items + kTeamWarps - 1) / kTeamWarps : p.items * p.team));
+    return launch_overlapped(kernel, grid, kTeamWarps * 32, smem, stream, std::max(p.team, 1), p);
   }
   const int groups = (int)(((long long)p.items + p.group - 1) / p.group);
   cudaError_t e = cudaSuccess;
   if (p.group > 1)
-    e = launch_overlapped(decode_walks_kernel, dim3((unsigned)groups), kWalkThreads, 0, stream, p);
+    e = launch_overlapped(decode_walks_kernel, dim3((unsigned)groups), kWalkThreads, 0, stream, 1, p);
   if (e == cudaSuccess)
     // one block saves the cluster's barriers as long as it describes all items at once
     e = groups <= kPlanAlone / p.lanes && p.group == 1
-            ? launch_overlapped(decode_plan_kernel<1>, dim3(1), kPlanAlone, 0, stream, p)
-            : launch_overlapped<kPlanBlocks>(decode_plan_kernel<kPlanBlocks>, dim3(kPlanBlocks), kPlanThreads, 0,
-                                             stream, p);
+            ? launch_overlapped(decode_plan_kernel<1>, dim3(1), kPlanAlone, 0, stream, 1, p)
+            : launch_overlapped(decode_plan_kernel<kPlanBlocks>, dim3(kPlanBlocks), kPlanThreads, 0, stream,
+                                kPlanBlocks, p);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(decode_kernel<D, HEADS, FMT>, dim3((unsigned)(p.warps / kDecWarps)),
-                        kDecWarps * 32, 0, stream, p);
+                        kDecWarps * 32, 0, stream, 1, p);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((p.warps + kJoinWarps - 1) / kJoinWarps), (unsigned)p.part_heads);
-  return launch_overlapped(decode_join_kernel<D>, grid, kJoinThreads, 0, stream, p);
+  const dim3 grid((unsigned)(p.join_items ? p.items : (p.warps + kJoinWarps - 1) / kJoinWarps),
+                  (unsigned)p.part_heads);
+  return launch_overlapped(decode_join_kernel<D>, grid, kJoinThreads, 0, stream, 1, p);
 }
 template <int D, int FMT>
 cudaError_t launch_decode_heads(const DecodeParams& p, cudaStream_t stream) {
@@ -1480,16 +1490,19 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   p.part = reinterpret_cast<float*>(take(lay.part));
   p.part_heads = std::min(p.G, p.heads);
   p.part_stride = p.part_heads * (d + 4);
-  // the most tiles that there can be: no more warps than have work
+  // the most tiles that an item can have, as far as the table goes
   const long long longest = (long long)max_pages * page_size;
-  double rows = 0;
-  for (int i = 0; i < npat; ++i) rows += (double)std::min<long long>(w[i], longest) / r[i] + 1;
-  const double tiles = (rows / kDecTile + npat) * p.items;
-  // a cluster for each item: as many items as surely run at once (two clusters in each of eight
-  // groups of SMs, at d = 64 twice that), none of more than eight tiles a warp
-  p.clusters = p.G <= 8 && p.items <= (d == 64 ? 32 : 16) && rows / kDecTile + npat <= kClusterTiles;
+  double tiles = 0;
+  for (int i = 0; i < npat; ++i) {
+    const long long n = (std::min<long long>(w[i], longest) + r[i] - 1) / r[i];
+    tiles += (double)((n + kDecTile - 1) / kDecTile);
+  }
+  p.team = decode_team(p.items, tiles, d, p.heads);
+  // no more warps than have work
   const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(p.G, d);
-  p.warps = kDecWarps * (int)std::min<double>(blocks, tiles * kSpreadWeight / (kDecWarps * kRangeWeight) + 1);
+  p.warps = kDecWarps * (int)std::min<double>(blocks, std::max(tiles, 1.0) * p.items * kSpreadWeight /
+                                                              (kDecWarps * kRangeWeight) + 1);
+  p.join_items = p.items <= p.warps / kJoinWarps;
   cudaError_t e;
   if (format == DILATTN_CACHE_E4M3)
     e = d == 64 ? launch_decode_heads<64, kFmtE4M3>(p, stream) : launch_decode_heads<128, kFmtE4M3>(p, stream);

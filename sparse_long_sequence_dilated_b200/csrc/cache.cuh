@@ -105,6 +105,57 @@ __device__ __forceinline__ void token_range(const CacheTokens& t, int b, int& lo
   n = e - a;
 }
 
+// The tokens of a page slot: rows r0 .. r0 + rows - 1 of `page`, from token
+// `tok` on; rows = 0 when the slot has none. The same in all lanes of a warp.
+// A sequence of n tokens touches at most floor(n / P) + 2 pages: sequence b, whose
+// first token is off, owns the slots from floor(off / P) + 2 b up to the next one's.
+// page = -1 (and the error word raised) for a position or page that there is not.
+struct PageRows {
+  int page, r0, rows, tok;
+};
+__device__ __forceinline__ PageRows page_rows(const CacheGeom& g, const CacheTokens& t, long long slot) {
+  const int lane = threadIdx.x & 31, P = 1 << g.lp;
+  PageRows pr{-1, 0, 0, 0};
+  int b = 0, off, n, start;
+  if (t.offsets != nullptr) {
+    // the slot's sequence: the last one whose first slot is at or before it
+    for (int span = g.B;;) {
+      const int step = (span + 31) / 32, at = b + lane * step;
+      int lo = 0, len = 0, st = 0;
+      if (lane * step < span) {
+        token_range(t, at, lo, len);
+        if (step == 1) st = t.start[at];
+      }
+      const bool in = lane * step < span && (lo >> g.lp) + 2ll * at <= slot;
+      const int k = max(__popc(__ballot_sync(0xffffffffu, in)) - 1, 0);
+      b += k * step;
+      if (step == 1) {
+        off = __shfl_sync(0xffffffffu, lo, k);
+        n = __shfl_sync(0xffffffffu, len, k);
+        start = __shfl_sync(0xffffffffu, st, k);
+        break;
+      }
+      span = min(step, span - k * step);
+    }
+  } else {
+    b = (int)min(slot, (long long)g.B - 1);
+    token_range(t, b, off, n);
+    start = t.start[b];
+  }
+  const bool good = start >= 0 && start <= 0x7fffffff - n;
+  if (!good) start = 0;
+  const long long skip = slot - (t.offsets != nullptr ? (off >> g.lp) + 2ll * b : b);
+  const long long row0 = ((long long)(start >> g.lp) + skip) << g.lp;
+  const long long lo = max((long long)start, row0), hi = min((long long)start + n, row0 + P);
+  if (n == 0 || lo >= hi) return pr;
+  if (good) pr.page = page_of(g, b, (int)lo);
+  else g.err.raise(kErrBadPage);
+  pr.r0 = (int)(lo - row0);
+  pr.rows = (int)(hi - lo);
+  pr.tok = off + (int)(lo - start);
+  return pr;
+}
+
 struct CacheWriteParams {
   CacheGeom geom;
   CacheTokens tok;
@@ -112,6 +163,8 @@ struct CacheWriteParams {
   long long stride[2];
   uint8_t* codes[2];
   float* scale[2];
+  uint32_t h_mul;             // reciprocal of Hkv (divisor_magic)
+  int h_sh;
 };
 
 // Largest magnitude of eight bf16 numbers, as their bits compare: infinities and NaN are 0x7f80 and above.
@@ -154,60 +207,6 @@ __device__ __forceinline__ void rescale_rows(uint8_t* codes, int P, int r0, int 
   }
 }
 
-// The new rows of a page slot: rows r0 .. r0 + rows - 1 of `page`, from token
-// `tok` on; rows = 0 when the slot has none. The same in all lanes of a warp.
-// A sequence of n tokens touches at most floor(n / P) + 2 pages: sequence b, whose
-// first token is off, owns the slots from floor(off / P) + 2 b up to the next one's.
-struct PageRows {
-  int page, r0, rows, tok;
-};
-__device__ __forceinline__ PageRows page_rows(const CacheWriteParams& p, long long slot) {
-  const int lane = threadIdx.x & 31, P = 1 << p.geom.lp;
-  PageRows pr{0, 0, 0, 0};
-  int b = 0, off, n, start;
-  if (p.tok.offsets != nullptr) {
-    // the slot's sequence: the last one whose first slot is at or before it
-    for (int span = p.geom.B;;) {
-      const int step = (span + 31) / 32, at = b + lane * step;
-      int lo = 0, len = 0, st = 0;
-      if (lane * step < span) {
-        token_range(p.tok, at, lo, len);
-        if (step == 1) st = p.tok.start[at];
-      }
-      const bool in = lane * step < span && (lo >> p.geom.lp) + 2ll * at <= slot;
-      const int k = max(__popc(__ballot_sync(0xffffffffu, in)) - 1, 0);
-      b += k * step;
-      if (step == 1) {
-        off = __shfl_sync(0xffffffffu, lo, k);
-        n = __shfl_sync(0xffffffffu, len, k);
-        start = __shfl_sync(0xffffffffu, st, k);
-        break;
-      }
-      span = min(step, span - k * step);
-    }
-  } else {
-    b = (int)min(slot, (long long)p.geom.B - 1);
-    token_range(p.tok, b, off, n);
-    start = p.tok.start[b];
-  }
-  if (n == 0) return pr;
-  if (start < 0 || start > 0x7fffffff - n) {
-    p.geom.err.raise(kErrBadPage);
-    return pr;
-  }
-  const long long skip = slot - (p.tok.offsets != nullptr ? (off >> p.geom.lp) + 2ll * b : b);
-  const long long row0 = ((long long)(start >> p.geom.lp) + skip) << p.geom.lp;
-  const long long lo = max((long long)start, row0), hi = min((long long)start + n, row0 + P);
-  if (lo >= hi) return pr;
-  const int page = page_of(p.geom, b, (int)lo);
-  if (page < 0) return pr;
-  pr.page = page;
-  pr.r0 = (int)(lo - row0);
-  pr.rows = (int)(hi - lo);
-  pr.tok = off + (int)(lo - start);
-  return pr;
-}
-
 // Few tokens of each sequence: a warp for each (touched page, KV head, K or V).
 // A page's first four new rows stay in registers, others are read twice.
 template <int D, int FMT>
@@ -215,13 +214,14 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
   constexpr int C = D / 64;  // 32-bit words of two numbers that a lane has of a row
   constexpr int KEEP = 4;
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int h = (int)(unit % p.geom.Hkv);
-  const int z = (int)(unit / p.geom.Hkv) & 1;
+  const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const uint32_t sz = udiv(unit, p.h_mul, p.h_sh);
+  const int h = (int)(unit - sz * (uint32_t)p.geom.Hkv);
+  const int z = (int)sz & 1;
   grid_dependency_wait();
   grid_dependency_release();
-  const PageRows pr = page_rows(p, unit / p.geom.Hkv >> 1);
-  if (pr.rows == 0) return;
+  const PageRows pr = page_rows(p.geom, p.tok, sz >> 1);
+  if (pr.rows == 0 || pr.page < 0) return;
   const __nv_bfloat16* x = p.x[z] + (long long)pr.tok * p.stride[z] + (long long)h * D;
   const size_t blk = (size_t)pr.page * p.geom.Hkv + h;
   uint8_t* codes = p.codes[z] + (blk << p.geom.lp) * D;
@@ -277,65 +277,68 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
   if (lane == 0) *scale = now;
 }
 
-// Ragged stretches: W warps for each (touched page, KV head, K or V), with all
-// of its new rows in registers, 64 numbers a lane, so that they are read once.
+// Ragged stretches: W warps for each (touched page, KV head), K and then V, with
+// all of its new rows in registers, 64 numbers a lane, so that they are read once.
 // Heads are the fastest index: blocks that run together read whole rows.
 template <int D, int FMT, int W>
 __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
   constexpr int V = D / 16;  // pieces of 16 numbers of a row
-  __shared__ uint32_t s_amax[8];
+  __shared__ uint32_t s_amax[2][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tid = threadIdx.x % (W * 32);  // in the unit
-  const long long unit = (long long)blockIdx.x * (8 / W) + warp / W;
-  const int h = (int)(unit % p.geom.Hkv);
-  const int z = (int)(unit / p.geom.Hkv) & 1;
+  const uint32_t unit = blockIdx.x * (8 / W) + warp / W;
+  const uint32_t slot = udiv(unit, p.h_mul, p.h_sh);
+  const int h = (int)(unit - slot * (uint32_t)p.geom.Hkv);
   const int P = 1 << p.geom.lp;
   grid_dependency_wait();
   grid_dependency_release();
-  const PageRows pr = page_rows(p, unit / p.geom.Hkv >> 1);
-  const bool work = pr.rows > 0;
-  const int r0 = pr.r0, rows = pr.rows;
-  const __nv_bfloat16* x = p.x[z] + (long long)pr.tok * p.stride[z] + (long long)h * D;
-  const size_t blk = (size_t)pr.page * p.geom.Hkv + h;
-  uint8_t* codes = p.codes[z] + (blk << p.geom.lp) * D;
-  float* scale = p.scale[z] + blk;
-  uint4 u[4][2];
-  uint32_t amax = 0;
+  const PageRows pr = page_rows(p.geom, p.tok, slot);
+  const bool work = pr.rows > 0 && pr.page >= 0;
+  const int r0 = pr.r0, rows = work ? pr.rows : 0;
+  const size_t blk = work ? (size_t)pr.page * p.geom.Hkv + h : 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = tid + i * W * 32;
-    u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
-    if (k / V < rows) {
-      const uint4* src = reinterpret_cast<const uint4*>(x + (long long)(k / V) * p.stride[z] + (k % V) * 16);
-      u[i][0] = src[0], u[i][1] = src[1];
+  for (int z = 0; z < 2; ++z) {
+    const __nv_bfloat16* x = p.x[z] + (long long)pr.tok * p.stride[z] + (long long)h * D;
+    uint8_t* codes = p.codes[z] + (blk << p.geom.lp) * D;
+    float* scale = p.scale[z] + blk;
+    uint4 u[4][2];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = tid + i * W * 32;
+      u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
+      if (k / V < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + (long long)(k / V) * p.stride[z] + (k % V) * 16);
+        u[i][0] = src[0], u[i][1] = src[1];
+      }
     }
-  }
-  const float was = work && r0 > 0 ? *scale : 0.f;
+    const float was = work && r0 > 0 ? *scale : 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) amax = max_magnitude(max_magnitude(amax, u[i][0]), u[i][1]);
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  if constexpr (W > 1) {
-    if (lane == 0) s_amax[warp] = amax;
-    __syncthreads();
-    const int first = warp / W * W;
+    for (int i = 0; i < 4; ++i) amax = max_magnitude(max_magnitude(amax, u[i][0]), u[i][1]);
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if constexpr (W > 1) {
+      if (lane == 0) s_amax[z][warp] = amax;
+      __syncthreads();
+      const int first = warp / W * W;
 #pragma unroll
-    for (int i = 0; i < W; ++i) amax = max(amax, s_amax[first + i]);
-  }
-  if (!work) return;
-  const float now = next_scale<FMT>(amax, was);
-  const bool poisoned = now != now;
-  const float inv = poisoned ? 0.f : 1.f / now;
-  if (r0 > 0 && now > was) rescale_rows<D, FMT>(codes, P, r0, r0 + rows, was * inv, tid, W * 32);
+      for (int i = 0; i < W; ++i) amax = max(amax, s_amax[z][first + i]);
+    }
+    if (!work) continue;
+    const float now = next_scale<FMT>(amax, was);
+    const bool poisoned = now != now;
+    const float inv = poisoned ? 0.f : 1.f / now;
+    if (r0 > 0 && now > was) rescale_rows<D, FMT>(codes, P, r0, r0 + rows, was * inv, tid, W * 32);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = tid + i * W * 32;
-    if (k / V >= rows) continue;
-    if (poisoned) u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(codes + (size_t)r0 * D + (size_t)k * 16) =
-        make_uint4(encode_bf16x4<FMT>(u[i][0].x, u[i][0].y, inv), encode_bf16x4<FMT>(u[i][0].z, u[i][0].w, inv),
-                   encode_bf16x4<FMT>(u[i][1].x, u[i][1].y, inv), encode_bf16x4<FMT>(u[i][1].z, u[i][1].w, inv));
+    for (int i = 0; i < 4; ++i) {
+      const int k = tid + i * W * 32;
+      if (k / V >= rows) continue;
+      if (poisoned) u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(codes + (size_t)r0 * D + (size_t)k * 16) =
+          make_uint4(encode_bf16x4<FMT>(u[i][0].x, u[i][0].y, inv), encode_bf16x4<FMT>(u[i][0].z, u[i][0].w, inv),
+                     encode_bf16x4<FMT>(u[i][1].x, u[i][1].y, inv), encode_bf16x4<FMT>(u[i][1].z, u[i][1].w, inv));
+    }
+    if (tid == 0) *scale = now;
   }
-  if (tid == 0) *scale = now;
 }
 
 struct CacheReadParams {
@@ -345,59 +348,107 @@ struct CacheReadParams {
   long long stride[2];
   const uint8_t* codes[2];
   const float* scale[2];
+  int pieces;                 // of 16 codes that a token has
+  uint32_t p_mul;             // reciprocal of pieces (divisor_magic)
+  int p_sh;
 };
 
-// One thread per 16 codes of a token and KV head.
-template <int D, int FMT>
-__global__ void __launch_bounds__(256) cache_read_kernel(const __grid_constant__ CacheReadParams p) {
+constexpr int kReadThreads = 256;
+
+// The last sequence whose first token is at or before tok. One warp.
+__device__ __forceinline__ int sequence_of(const CacheReadParams& p, long long tok) {
+  int b = 0;
+  for (int span = p.geom.B; span > 1;) {
+    const int lane = threadIdx.x & 31, step = (span + 31) / 32, at = b + lane * step;
+    const bool in = lane * step < span && p.tok.offsets[at] <= tok;
+    const int k = max(__popc(__ballot_sync(0xffffffffu, in)) - 1, 0);
+    b += k * step;
+    span = min(step, span - k * step);
+  }
+  return b;
+}
+
+// A block has kReadThreads * EACH successive pieces of 16 codes, in the order of the rows that
+// it writes: they are two thirds of the traffic. Two warps find the sequences of its first and
+// its last token; a thread's own lies between them.
+template <int D, int FMT, int EACH>
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ CacheReadParams p) {
   constexpr int V = D / 16;
-  const long long per = (long long)p.geom.Hkv * V;
-  const long long total = per * p.tok.T;
-  const int z = blockIdx.z;
+  __shared__ int s_seq[2];
+  const int tid = threadIdx.x, warp = tid >> 5, z = blockIdx.y;
+  const long long first = (long long)blockIdx.x * (kReadThreads * EACH);
+  const long long tok0 = first / p.pieces;
+  const uint32_t skip = (uint32_t)(first - tok0 * p.pieces);
   grid_dependency_wait();
   grid_dependency_release();
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (long long)gridDim.x * 256) {
-    const int tok = (int)(i / per), rest = (int)(i % per);
-    const int h = rest / V, c = rest % V;
-    // last sequence whose first token is at or before tok
-    int b = tok;
-    if (p.tok.offsets != nullptr) {
-      int a = 0, e = p.geom.B;
-      while (e - a > 1) {
-        const int m = (a + e) >> 1;
-        if (p.tok.offsets[m] <= tok) a = m; else e = m;
-      }
-      b = a;
+  if (p.tok.offsets != nullptr) {
+    if (warp < 2) {
+      const long long last = min(tok0 + udiv(skip + kReadThreads * EACH - 1, p.p_mul, p.p_sh), (long long)p.tok.T - 1);
+      const int b = sequence_of(p, warp == 0 ? tok0 : last);
+      if ((tid & 31) == 0) s_seq[warp] = b;
     }
-    if (b >= p.geom.B) continue;
+    __syncthreads();
+  }
+  long long tok[EACH], row[EACH];  // row < 0: reads as zeros
+  size_t blk[EACH];
+  uint32_t piece[EACH];
+  bool real[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const uint32_t j = skip + tid + i * kReadThreads, dt = udiv(j, p.p_mul, p.p_sh);
+    tok[i] = tok0 + dt;
+    piece[i] = j - dt * (uint32_t)p.pieces;
+    real[i] = tok[i] < p.tok.T;
+    row[i] = -1;
+    blk[i] = 0;
+    if (!real[i]) continue;
+    int b = (int)tok[i];
+    if (p.tok.offsets != nullptr) {
+      b = s_seq[0];
+      for (int e = s_seq[1] + 1; e - b > 1;) {
+        const int m = (b + e) >> 1;
+        if (p.tok.offsets[m] <= tok[i]) b = m; else e = m;
+      }
+    }
     int off, n;
     token_range(p.tok, b, off, n);
-    if (tok < off || tok >= off + n) continue;
-    const long long pos = (long long)p.tok.start[b] + tok - off;
+    real[i] = b < p.geom.B && tok[i] >= off && tok[i] < off + n;
+    if (!real[i]) continue;
+    const long long pos = (long long)p.tok.start[b] + tok[i] - off;
     int page = -1;
     if (pos >= 0 && pos <= 0x7fffffff) page = page_of(p.geom, b, (int)pos);
     else p.geom.err.raise(kErrBadPage);
-    uint4 u = make_uint4(0, 0, 0, 0);
-    float s = 0.f;
     if (page >= 0) {
-      const size_t blk = (size_t)page * p.geom.Hkv + h;
-      const size_t row = (blk << p.geom.lp) + (pos & ((1 << p.geom.lp) - 1));
-      u = *reinterpret_cast<const uint4*>(p.codes[z] + row * D + c * 16);
-      s = p.scale[z][blk];
+      blk[i] = (size_t)page * p.geom.Hkv + piece[i] / V;
+      row[i] = (long long)((blk[i] << p.geom.lp) + (size_t)(pos & ((1 << p.geom.lp) - 1)));
     }
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  }
+  uint4 u[EACH];
+  float sc[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    u[i] = make_uint4(0, 0, 0, 0);
+    sc[i] = 0.f;
+    if (row[i] >= 0) {
+      u[i] = *reinterpret_cast<const uint4*>(p.codes[z] + (size_t)row[i] * D + (piece[i] % V) * 16);
+      sc[i] = p.scale[z][blk[i]];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    if (!real[i]) continue;
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
     uint32_t o[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float f[4];
       decode4<FMT>(w[j], f);
-      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0] * s, f[1] * s);
-      const __nv_bfloat162 e = __floats2bfloat162_rn(f[2] * s, f[3] * s);
+      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0] * sc[i], f[1] * sc[i]);
+      const __nv_bfloat162 e = __floats2bfloat162_rn(f[2] * sc[i], f[3] * sc[i]);
       o[2 * j] = *reinterpret_cast<const uint32_t*>(&a);
       o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&e);
     }
-    uint4* dst = reinterpret_cast<uint4*>(p.x[z] + (long long)tok * p.stride[z] + h * D + c * 16);
+    uint4* dst = reinterpret_cast<uint4*>(p.x[z] + tok[i] * p.stride[z] + (long long)piece[i] * 16);
     dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }

@@ -1170,9 +1170,11 @@ cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, s
 }
 
 template <int D, int FMT>
-cudaError_t launch_cache_write(const CacheWriteParams& p, long long units, int page_size, cudaStream_t stream) {
+cudaError_t launch_cache_write(const CacheWriteParams& p, long long slots, int page_size, cudaStream_t stream) {
+  const long long units = slots * p.geom.Hkv;
   if (p.tok.offsets == nullptr || p.tok.T <= 8 * (long long)p.geom.B)
-    return launch_overlapped(cache_append_kernel<D, FMT>, dim3((unsigned)((units + 7) / 8)), 256, 0, stream, 1, p);
+    return launch_overlapped(cache_append_kernel<D, FMT>, dim3((unsigned)((2 * units + 7) / 8)), 256, 0, stream, 1,
+                             p);
   // 64 numbers a lane
   const int warps = std::max(1, page_size * D / 2048);
   const dim3 grid((unsigned)((units * warps + 7) / 8));
@@ -1181,6 +1183,17 @@ cudaError_t launch_cache_write(const CacheWriteParams& p, long long units, int p
                       : warps == 4 ? cache_write_kernel<D, FMT, 4>
                                    : cache_write_kernel<D, FMT, D / 16>;
   return launch_overlapped(kernel, grid, 256, 0, stream, 1, p);
+}
+
+template <int D, int FMT>
+cudaError_t launch_cache_read(const CacheReadParams& p, int num_sms, cudaStream_t stream) {
+  // one piece a thread while every thread runs at once (3 against 3.6 us for a few tokens), then
+  // two, whose loads overlap (506 against 590 us for 131072 tokens of 32 heads, d = 128)
+  const long long all = (long long)p.tok.T * p.pieces;
+  const int each = all <= 2048ll * num_sms ? 1 : 2;
+  const dim3 grid((unsigned)((all + kReadThreads * each - 1) / (kReadThreads * each)), 2);
+  const auto kernel = each == 1 ? cache_read_kernel<D, FMT, 1> : cache_read_kernel<D, FMT, 2>;
+  return launch_overlapped(kernel, grid, kReadThreads, 0, stream, 1, p);
 }
 
 // Whether a written buffer overlaps a read one.
@@ -1228,15 +1241,15 @@ extern "C" int dilattn_cache_write(const void* k, const void* v, long long k_str
   p.scale[0] = ks;
   p.scale[1] = vs;
   const long long slots = offsets == nullptr ? B : (long long)T / page_size + 2ll * B + 1;
-  const double units = (double)slots * Hkv * 2;
-  if (units * 8 > 2147483647.0) return DILATTN_ERR_UNSUPPORTED;
+  if ((double)slots * Hkv * 8 > 2147483647.0) return DILATTN_ERR_UNSUPPORTED;
+  divisor_magic((uint32_t)Hkv, p.h_mul, p.h_sh);
   cudaError_t e;
   if (format == DILATTN_CACHE_E4M3)
-    e = d == 64 ? launch_cache_write<64, kFmtE4M3>(p, (long long)units, page_size, stream)
-                : launch_cache_write<128, kFmtE4M3>(p, (long long)units, page_size, stream);
+    e = d == 64 ? launch_cache_write<64, kFmtE4M3>(p, slots, page_size, stream)
+                : launch_cache_write<128, kFmtE4M3>(p, slots, page_size, stream);
   else
-    e = d == 64 ? launch_cache_write<64, kFmtInt8>(p, (long long)units, page_size, stream)
-                : launch_cache_write<128, kFmtInt8>(p, (long long)units, page_size, stream);
+    e = d == 64 ? launch_cache_write<64, kFmtInt8>(p, slots, page_size, stream)
+                : launch_cache_write<128, kFmtInt8>(p, slots, page_size, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
   return DILATTN_OK;
 }
@@ -1274,13 +1287,17 @@ extern "C" int dilattn_cache_read(const void* kc, const void* vc, const float* k
   p.codes[1] = reinterpret_cast<const uint8_t*>(vc);
   p.scale[0] = ks;
   p.scale[1] = vs;
-  const long long pieces = (long long)T * Hkv * (d / 16);
-  const dim3 grid((unsigned)std::min<long long>((pieces + 255) / 256, (long long)st->num_sms * 64),
-                  1, 2);
-  const auto kernel = format == DILATTN_CACHE_E4M3
-                          ? (d == 64 ? cache_read_kernel<64, kFmtE4M3> : cache_read_kernel<128, kFmtE4M3>)
-                          : (d == 64 ? cache_read_kernel<64, kFmtInt8> : cache_read_kernel<128, kFmtInt8>);
-  const cudaError_t e = launch_overlapped(kernel, grid, 256, 0, stream, 1, p);
+  const long long most = (long long)Hkv * (d / 16);
+  if (most > 0x3fffffffLL || (double)T * most / kReadThreads > 2147483647.0) return DILATTN_ERR_UNSUPPORTED;
+  p.pieces = (int)most;
+  divisor_magic((uint32_t)p.pieces, p.p_mul, p.p_sh);
+  cudaError_t e;
+  if (format == DILATTN_CACHE_E4M3)
+    e = d == 64 ? launch_cache_read<64, kFmtE4M3>(p, st->num_sms, stream)
+                : launch_cache_read<128, kFmtE4M3>(p, st->num_sms, stream);
+  else
+    e = d == 64 ? launch_cache_read<64, kFmtInt8>(p, st->num_sms, stream)
+                : launch_cache_read<128, kFmtInt8>(p, st->num_sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "cache_read_kernel launch");
   return DILATTN_OK;
 }
@@ -1297,16 +1314,17 @@ long long decode_items(int T, int Hkv, int G) {
 int decode_blocks_per_sm(int G, int d) { return G > 8 ? 2 : d == 64 ? 4 : 3; }
 
 // Blocks of a team for `items` items of up to `tiles` tiles (see decode_team_kernel), or -1: they
-// are too many or too long, and ranges of all items' tiles serve better. A warp does up to eight
-// tiles in the time that the plan and the join would take; teams of blocks all run at once, in
-// eight groups of 16 or more SMs with one block on each (two at d = 64 and up to 8 heads), and
-// the larger the sooner they are done.
+// are too many or too long, and ranges of all items' tiles serve better. Up to eight tiles are
+// done by a warp before more of them would have met. Teams of blocks all run at once, in eight
+// groups of 16 or more SMs with one block on each (two at d = 64 and up to 8 heads); the larger
+// the sooner they are done. Where they do not fit, a warp does 16 tiles in about the time that
+// the plan and the join take.
 int decode_team(int items, double tiles, int d, int heads) {
   if (tiles <= 8) return 0;
   const int each = d == 64 && heads <= 8 ? 2 : 1;
   for (int team = kTeamBlocks; team >= 1; team /= 2)
     if (tiles <= 8 * kTeamWarps * team && (double)items * team <= 128 * each) return team;
-  return -1;
+  return tiles <= 16 ? 0 : -1;
 }
 
 // Workspace of a decode: the items' walks, the warps' ranges, and the partials of cut items.

@@ -1030,25 +1030,32 @@ __global__ void __launch_bounds__(kTeamWarps * 32, D == 64 && HEADS <= 8 ? 2 : 1
   __syncthreads();
   const DecodeItem it = item_of(p, item);
   const int pieces = it.nh * (D / 4);
-  // element piece i of `n` partials, the k-th one at part(k); those whose mark is 0 are not there
+  // element piece i of up to eight partials, the k-th one at part(k); those whose mark is 0 are not there
   auto join = [&](auto part, int n, int i, float& M, float& MV, float& L) {
     const int hl = i / (D / 4);
+    float4 st[8], x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      st[k] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+      if (k < n) {
+        st[k] = *reinterpret_cast<const float4*>(part(k) + stat + hl * 4);
+        x[k] = reinterpret_cast<const float4*>(part(k))[i];
+      }
+    }
     M = MV = kNoMax;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) M = fmaxf(M, st[k].x), MV = fmaxf(MV, st[k].y);
     L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < n; ++k) {
-      const float4 st = *reinterpret_cast<const float4*>(part(k) + stat + hl * 4);
-      M = fmaxf(M, st.x);
-      MV = fmaxf(MV, st.y);
-    }
-    for (int k = 0; k < n; ++k) {
-      const float4 st = *reinterpret_cast<const float4*>(part(k) + stat + hl * 4);
-      if (st.w == 0.f) continue;
-      L += st.z * exp2f(st.x - M);
-      add_scaled(a, reinterpret_cast<const float4*>(part(k))[i], exp2f(st.y - MV));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (st[k].w == 0.f) continue;
+      L += st[k].z * exp2f(st[k].x - M);
+      add_scaled(a, x[k], exp2f(st[k].y - MV));
     }
     return a;
   };
+  static_assert(kTeamWarps <= 8 && kTeamBlocks <= 8, "join takes eight");
   for (int i = tid; i < pieces; i += kTeamWarps * 32) {
     float M, MV, L;
     reinterpret_cast<float4*>(s_block)[i] =

@@ -14,6 +14,11 @@
 // walk ends there; what overlap remains (r that do not divide one another) is
 // masked row by row. An item's walks, in tiles of 32 rows, are its work.
 //
+// Dense attention of several tokens to a sequence (drafted tokens) reads the
+// same rows for all of them. There an item has p.tokens successive tokens, whose
+// heads side by side are its columns, and a walk for each sequence among them;
+// a row counts for the columns of its sequence whose token is not before it.
+//
 // Split. The tiles of all items form one sequence that is cut into contiguous
 // ranges of equal weight, one for each warp of a persistent grid, wherever the cut
 // falls: no batch shape, length or head count leaves SMs idle. Warps do not
@@ -57,7 +62,8 @@ struct __align__(8) DecodeRange {
   int item, tile;
 };
 // One walk of an item: rows base + k r, k < n. s: the segment's start (the
-// largest int when no head of the item takes part); heads: bits of those that do.
+// largest int when no head of the item takes part; with p.tokens > 1 the
+// sequence); heads: bits of those that take part.
 struct __align__(16) DecodeWalk {
   int s, n, base;
   uint32_t heads;
@@ -90,7 +96,9 @@ struct DecodeParams {
   int join_items;            // decode_join_kernel has a block for each item, not for every 8 ranges
   float qk_scale;            // log2(e) / sqrt(d)
   int npat;                  // patterns, by ascending r
-  int dense;                 // one pattern with r = 1: every head takes every row of a walk
+  int dense;                 // one pattern with r = 1: every head of a token takes every row of a walk
+  int tokens;                // tokens of an item
+  int g_rec;                 // ceil(256 / G): i / G = i g_rec / 256 for i < 16, G <= 8
   int w[kMaxPat], r[kMaxPat];
   uint32_t w_mul[kMaxPat], r_mul[kMaxPat];
   int w_sh[kMaxPat], r_sh[kMaxPat];
@@ -123,11 +131,11 @@ struct DecodeCfg {
   static constexpr int BLOCKS_PER_SM = NB == 2 ? 2 : D == 64 ? 4 : 3;
 };
 
-// Where an item belongs.
+// Where an item belongs; nh: its columns. `tokens` is p.tokens, or 1 where that is known.
 struct DecodeItem {
   int token, hk, h0, nh;
 };
-__device__ __forceinline__ DecodeItem item_of(const DecodeParams& p, int item) {
+__device__ __forceinline__ DecodeItem item_of(const DecodeParams& p, int item, int tokens) {
   DecodeItem it;
   it.token = (int)udiv((uint32_t)item, p.pt_mul, p.pt_sh);
   const int c = item - it.token * p.per_token;
@@ -135,7 +143,21 @@ __device__ __forceinline__ DecodeItem item_of(const DecodeParams& p, int item) {
   const int first = (c - it.hk * p.nsub) * p.heads;
   it.h0 = it.hk * p.G + first;
   it.nh = min(p.heads, p.G - first);
+  if (tokens > 1) {
+    it.token *= tokens;
+    it.nh = min(tokens, p.T - it.token) * p.G;
+  }
   return it;
+}
+// The token of an item's column, and where in [T][H] its head lies.
+__device__ __forceinline__ int token_of(const DecodeParams& p, const DecodeItem& it, int column, int tokens) {
+  return it.token + (tokens > 1 ? column * p.g_rec >> 8 : 0);
+}
+__device__ __forceinline__ int head_of(const DecodeParams& p, const DecodeItem& it, int column, int tokens) {
+  return it.h0 + column - (tokens > 1 ? (column * p.g_rec >> 8) * p.G : 0);
+}
+__device__ __forceinline__ size_t place_of(const DecodeParams& p, const DecodeItem& it, int column, int tokens) {
+  return (size_t)token_of(p, it, column, tokens) * p.H + head_of(p, it, column, tokens);
 }
 
 // ---------------------------------------------------------------------------
@@ -188,11 +210,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // of a warp work on an item, lane j of them on pattern j; all 32 take part.
 __device__ int describe_item(const DecodeParams& p, int item, DecodeHead* head, DecodeWalk* walk) {
   const bool real = item < p.items;
-  const DecodeItem it = item_of(p, real ? item : 0);
+  const DecodeItem it = item_of(p, real ? item : 0, p.tokens);
   const int j = threadIdx.x & (p.lanes - 1), jj = min(j, p.npat - 1);
+  const int token = it.token + (p.tokens > 1 ? j : 0);
   DecodeHead hd;
-  hd.b = p.seq != nullptr ? p.seq[it.token] : it.token;
-  hd.pos = p.pos[it.token];
+  hd.b = 0;
+  hd.pos = -1;
+  if (token < p.T && (p.tokens == 1 || j < p.tokens)) {  // lanes may be more than the tokens
+    hd.b = p.seq != nullptr ? p.seq[token] : token;
+    hd.pos = p.pos[token];
+  }
   hd.pad = 0;
   const int r = p.r[jj], w = p.w[jj], r_sh = p.r_sh[jj];
   const uint32_t r_mul = p.r_mul[jj], w_mul = p.w_mul[jj], div = p.divisors[jj];
@@ -205,8 +232,25 @@ __device__ int describe_item(const DecodeParams& p, int item, DecodeHead* head, 
   }
   if (hd.pos < 0) hd.b = 0;
   DecodeWalk wk{0x7fffffff, 0, 0, 0u};
+  if (p.tokens > 1) {  // the first token of a sequence walks for all
+    bool first = hd.pos >= 0;
+    int top = -1;
+    for (int l = 0; l < p.lanes; ++l) {
+      const int bl = __shfl_sync(0xffffffffu, hd.b, l, p.lanes), pl = __shfl_sync(0xffffffffu, hd.pos, l, p.lanes);
+      if (bl != hd.b || pl < 0) continue;
+      first = first && l >= j;
+      top = max(top, pl);
+      wk.heads |= ((1u << p.G) - 1) << (l * p.G);
+    }
+    if (first) {
+      wk.s = hd.b;
+      wk.n = top + 1;
+    } else {
+      wk.heads = 0;
+    }
+  }
   int s = 0;
-  if (hd.pos >= 0 && j < p.npat) {
+  if (p.tokens == 1 && hd.pos >= 0 && j < p.npat) {
     s = (int)udiv((uint32_t)hd.pos, w_mul, w_sh) * w;
     const int rel = hd.pos - s;
     const int steps = (int)udiv((uint32_t)rel, r_mul, r_sh);
@@ -224,12 +268,12 @@ __device__ int describe_item(const DecodeParams& p, int item, DecodeHead* head, 
     }
   }
   int limit = 0x7fffffff;
-  for (int l = 0; l + 1 < p.npat; ++l) {
+  for (int l = 0; l + 1 < p.npat && p.tokens == 1; ++l) {
     const int sl = __shfl_sync(0xffffffffu, s, l, p.lanes);
     const uint32_t hl = __shfl_sync(0xffffffffu, wk.heads, l, p.lanes);
     if ((div >> l & 1u) && (wk.heads & ~hl) == 0) limit = min(limit, sl);
   }
-  if (wk.n > 0 && limit <= hd.pos)
+  if (p.tokens == 1 && wk.n > 0 && limit <= hd.pos)
     wk.n = limit > wk.base ? (int)udiv((uint32_t)(limit - 1 - wk.base), r_mul, r_sh) + 1 : 0;
   if (real && j < p.npat) walk[j] = wk;
   int tiles = (int)(((uint32_t)wk.n + kDecTile - 1) / kDecTile);
@@ -461,7 +505,8 @@ __device__ __forceinline__ float final_lse(float m, float l) {
 // walk[0] from item first_item on; part: the warp's two slots for partials, slot_stride
 // floats apart; qf, s_walk: shared memory of the warp (the lane's own fragments
 // of Q, NB * MT of them 32 apart, and the walks of the item to fetch from).
-template <int D, int HEADS, int FMT>
+// GROUPED: p.tokens > 1.
+template <int D, int HEADS, int FMT, bool GROUPED>
 __device__ __forceinline__ void decode_range(const DecodeParams& p, const DecodeRange rg, const DecodeRange end,
                                              const DecodeHead* head, const DecodeWalk* walk, int first_item,
                                              float* part, size_t slot_stride, uint2* qf, DecodeWalk* s_walk) {
@@ -470,6 +515,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
   constexpr int HW = HEADS < 8 ? HEADS : 8;        // heads of an MMA's columns
   constexpr int VR = HW <= 2 ? 1 : HW / 2;         // rows of a tile that a lane's softmax has
   constexpr int VE = HW == 1 ? 1 : 2;              // heads of them, for each NB
+  const int tokens_of_item = GROUPED ? p.tokens : 1;
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int row_l = 8 * c + g;                     // the row this lane looks up
@@ -479,13 +525,14 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
   // ---- the walk to fetch from (a_...), the looked-up tile (f_...), the tile in registers
   int a_item = rg.item, a_tiles, a_pos, a_hk, a_b, a_j, a_n, a_base, a_r;  // a_tiles: of the item, in the range
   uint32_t a_k, a_walks, a_in;  // patterns with rows to walk; patterns of the item's head (HEADS = 1)
-  int f_page = -1, f_x = 0, f_hk = 0;
+  int f_page = -1, f_x = 0, f_hk = 0, f_j = 0;
   uint32_t f_meta = 0;
   bool a_some = true, f_some = false, f_whole = false;
 
   auto set_walk = [&](int j) {
     const DecodeWalk wk = s_walk[j];
     a_j = j;
+    if constexpr (GROUPED) a_b = wk.s;
     a_n = wk.n;
     a_base = wk.base;
     a_r = p.r[j];
@@ -496,7 +543,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
     const DecodeHead hd = head[item - first_item];
     a_pos = hd.pos;
     a_b = hd.b;
-    a_hk = item_of(p, item).hk;
+    a_hk = item_of(p, item, tokens_of_item).hk;
     a_tiles = item == end.item ? end.tile : hd.tiles;
     a_walks = __ballot_sync(0xffffffffu, wk.n > 0);
     a_in = __ballot_sync(0xffffffffu, wk.heads & 1u);
@@ -514,6 +561,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
     if (!f_some) return;
     const uint32_t k = a_k + row_l, n = (uint32_t)a_n;  // k may pass 2^31 in the last tile
     f_hk = a_hk;
+    f_j = a_j;
     f_page = -1;
     f_meta = 0;
     const int x0 = (int)((uint32_t)a_base + a_k * (uint32_t)a_r);
@@ -522,8 +570,8 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
       f_x = x0 + row_l * a_r;
       f_page = p.geom.table[(size_t)a_b * p.geom.max_pages + (f_x >> p.geom.lp)];
     }
-    if (p.dense) {
-      f_meta = k < n ? 0x10001u : 0u;
+    if (GROUPED || p.dense) {
+      f_meta = k < n ? (GROUPED ? (uint32_t)f_x + 1 : 1u) : 0u;
     } else {
       // patterns that hold the row: low half; the one that walks it and all before: high half
       const int last = (int)((uint32_t)a_base + min(a_k + kDecTile - 1, n - 1) * (uint32_t)a_r);
@@ -551,7 +599,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
       }
     } else if (a_k >= n) {
       a_k = 0;
-      set_walk(__ffs(a_walks & ~((2u << a_j) - 1)) - 1);
+      set_walk(max(__ffs(a_walks & ~((2u << a_j) - 1)) - 1, 0));
     }
   };
   constexpr int KQ = D / 64, VW = D / 32;  // 16-byte pieces of a K row, words of a V row, that a lane holds
@@ -559,6 +607,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
   const uint8_t* const base_v = p.codes[1] + g * (D / 8);
   uint32_t row = 0, meta_l = 0;  // this lane's row of the cache, and what f_meta said of it
   float ks_l = 0.f, vs_l = 0.f;
+  int walk_l = 0;
   bool whole = false, any = false;
   uint4 kr[4][KQ];
   uint32_t vr[8][VW];
@@ -573,6 +622,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
     ks_l = p.scale[0][blk];
     vs_l = p.scale[1][blk];
     meta_l = in ? f_meta : 0u;
+    walk_l = f_j;
     row = in ? (blk << p.geom.lp) + (uint32_t)(f_x & pmask) : 0u;
     const uint32_t ins = __ballot_sync(0xffffffffu, in);
     any = ins != 0;
@@ -618,18 +668,19 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
   int tiles;                 // its tiles from here on, in the range
   float acc[MT][NB][4];
   float m[2 * NB], mv[2 * NB], l[2 * NB], fac[2 * NB];  // of columns nb * 8 + 2 c + e
-  uint32_t in_pat[2 * NB];   // patterns that each of the lane's heads takes part in
+  uint32_t in_pat[2 * NB];   // walks that each of the lane's columns takes part in
+  int upto_pos[2 * NB];      // and their tokens' positions (p.tokens > 1)
   uint2 raw[NB][MT];  // q of head nb * 8 + g mod HW
   auto load_q = [&](int item) {
-    const DecodeItem it = item_of(p, item);
+    const DecodeItem it = item_of(p, item, tokens_of_item);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int hl = nb * 8 + (g & (HW - 1));
 #pragma unroll
       for (int k = 0; k < MT; ++k) {
         const int d0 = (k >> 2) * 64 + c * 16 + (k & 3) * 4;
-        raw[nb][k] = hl < it.nh ? *reinterpret_cast<const uint2*>(p.q + (long long)it.token * p.q_stride +
-                                                                  (it.h0 + hl) * D + d0)
+        raw[nb][k] = hl < it.nh ? *reinterpret_cast<const uint2*>(p.q + (long long)token_of(p, it, hl, tokens_of_item) * p.q_stride +
+                                                                  head_of(p, it, hl, tokens_of_item) * D + d0)
                                 : make_uint2(0, 0);
       }
     }
@@ -672,6 +723,11 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
         m[2 * nb + e2] = mv[2 * nb + e2] = kNoMax;
         l[2 * nb + e2] = 0.f;
         in_pat[2 * nb + e2] = 0;
+        upto_pos[2 * nb + e2] = 0;
+        if constexpr (GROUPED) {
+          const DecodeItem it = item_of(p, item, tokens_of_item);
+          upto_pos[2 * nb + e2] = p.pos[token_of(p, it, min(nb * 8 + 2 * c + e2, it.nh - 1), tokens_of_item)];
+        }
       }
       if constexpr (HEADS > 1) {
 #pragma unroll
@@ -692,7 +748,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
 
   // The item is done here (slot < 0: this warp had all of it), or a partial of it goes to the slot.
   auto end_item = [&](int item, int slot) {
-    const DecodeItem it = item_of(p, item);
+    const DecodeItem it = item_of(p, item, tokens_of_item);
     float* const dst = part + max(slot, 0) * slot_stride;
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i) {
@@ -708,7 +764,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
         if (hl >= it.nh) continue;
         if (slot < 0) {
           const float f = final_factor(m[i], mv[i], l[i]);
-          const size_t oi = (size_t)it.token * p.H + it.h0 + hl;
+          const size_t oi = place_of(p, it, hl, tokens_of_item);
           uint32_t o[D / 16];
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -793,6 +849,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
     float ks[VR], lv[VR];
     uint32_t meta[VR];
     const bool some = any;
+    const int walk_j = walk_l;
     {
       const float lv_l = fast_log2(vs_l);
 #pragma unroll
@@ -803,7 +860,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
           ks[v] = __shfl_sync(0xffffffffu, ks_l, from);
           lv[v] = __shfl_sync(0xffffffffu, lv_l, from);
         }
-        if (VR > 1 && !(whole && p.dense)) meta[v] = __shfl_sync(0xffffffffu, meta_l, from);
+        if (VR > 1 && (GROUPED || !(whole && p.dense))) meta[v] = __shfl_sync(0xffffffffu, meta_l, from);
       }
     }
     more = f_some;
@@ -836,7 +893,9 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
           cnt[v][nb][e] = 1.f;
           if constexpr (HEADS == 1) {
             cnt[v][nb][e] = (float)(meta[v] & 31u);
-          } else if (!p.dense) {
+          } else if (p.dense) {
+            if constexpr (GROUPED) ok = ok && (int)(meta[v] - 1) <= upto_pos[i] && (in_pat[i] >> walk_j & 1u);
+          } else {
             const uint32_t u = meta[v] & in_pat[i], upto = meta[v] >> 16;
             ok = ok && (u & upto) == (upto ^ (upto >> 1));
             cnt[v][nb][e] = (float)__popc(u);
@@ -940,7 +999,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
   }
 }
 
-template <int D, int HEADS, int FMT>
+template <int D, int HEADS, int FMT, bool GROUPED>
 __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>::BLOCKS_PER_SM))
     decode_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ uint2 s_q[kDecWarps][(HEADS + 7) / 8 * D / 16 * 32];
@@ -952,8 +1011,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>
   const DecodeRange rg = p.range[wi], end = p.range[wi + 1];
   grid_dependency_release();
   if (rg.item == end.item && rg.tile == end.tile) return;
-  decode_range<D, HEADS, FMT>(p, rg, end, p.head, p.walk, 0, p.part + (size_t)wi * 2 * p.part_stride, p.part_stride,
-                              s_q[warp] + lane, s_walk[warp]);
+  decode_range<D, HEADS, FMT, GROUPED>(p, rg, end, p.head, p.walk, 0, p.part + (size_t)wi * 2 * p.part_stride,
+                                       p.part_stride, s_q[warp] + lane, s_walk[warp]);
 }
 
 __device__ __forceinline__ void add_scaled(float4& a, const float4& x, float f) {
@@ -1022,13 +1081,14 @@ __global__ void __launch_bounds__(kTeamWarps * 32, D == 64 && HEADS <= 8 ? 2 : 1
     }
     float* const part = s_part + warp * p.part_stride;
     if (alone || rg.tile < end.tile)
-      decode_range<D, HEADS, FMT>(p, rg, end, &s_head[own], s_desc[own], item, part, 0, s_q[warp] + lane, s_walk[warp]);
+      decode_range<D, HEADS, FMT, false>(p, rg, end, &s_head[own], s_desc[own], item, part, 0, s_q[warp] + lane,
+                                         s_walk[warp]);
     else if (lane < p.part_heads)
       reinterpret_cast<float4*>(part + stat)[lane] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
   }
   if (alone) return;
   __syncthreads();
-  const DecodeItem it = item_of(p, item);
+  const DecodeItem it = item_of(p, item, p.tokens);
   const int pieces = it.nh * (D / 4);
   // element piece i of up to eight partials, the k-th one at part(k); those whose mark is 0 are not there
   auto join = [&](auto part, int n, int i, float& M, float& MV, float& L) {
@@ -1069,7 +1129,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32, D == 64 && HEADS <= 8 ? 2 : 1
     const float4 a = join([&](int k) { return (const float*)cluster.map_shared_rank(s_block, k); }, blocks, i,
                           M, MV, L);
     const int hl = i / (D / 4);
-    store_joined(p, D, (size_t)it.token * p.H + it.h0 + hl, i % (D / 4), a, M, MV, L);
+    store_joined(p, D, place_of(p, it, hl, p.tokens), i % (D / 4), a, M, MV, L);
   }
   cluster.sync();  // no block ends while another reads its sums
 }
@@ -1138,7 +1198,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __gr
     grid_dependency_release();
     __syncthreads();
     w = w_own;
-    const DecodeItem it = item_of(p, b.tile > 0 ? b.item : 0);
+    const DecodeItem it = item_of(p, b.tile > 0 ? b.item : 0, p.tokens);
     // an item begins in range w and goes on past it
     if (b.tile > 0 && (a.item != b.item || a.tile == 0) && hl < it.nh) {
       const uint32_t held = __ballot_sync(0xffffffffu, r.item == b.item);
@@ -1178,7 +1238,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __gr
           acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
           acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
         }
-        if (row == 0) store_joined(p, D, (size_t)it.token * p.H + it.h0 + hl, col, acc, M, MV, L);
+        if (row == 0) store_joined(p, D, place_of(p, it, hl, p.tokens), col, acc, M, MV, L);
       }
     }
     __syncthreads();
@@ -1192,7 +1252,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __gr
     }
     ++n;
   }
-  const DecodeItem it = item_of(p, p.join_items ? (int)blockIdx.x : range(w + 1).item);
+  const DecodeItem it = item_of(p, p.join_items ? (int)blockIdx.x : range(w + 1).item, p.tokens);
   if (hl >= it.nh) return;
   const float* first = p.part + ((size_t)w * 2 + 1) * p.part_stride;
   const float* rest = p.part + (size_t)(w + 1) * 2 * p.part_stride - step;
@@ -1240,7 +1300,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __gr
     float4 a = s_acc[0][tid];
 #pragma unroll
     for (int k = 1; k < kJoinThreads / LANES; ++k) add_scaled(a, s_acc[k][tid], 1.f);
-    store_joined(p, D, (size_t)it.token * p.H + it.h0 + hl, tid, a, M, MV, L);
+    store_joined(p, D, place_of(p, it, hl, p.tokens), tid, a, M, MV, L);
   }
 }
 

@@ -1305,13 +1305,19 @@ extern "C" int dilattn_cache_read(const void* kc, const void* vc, const float* k
 namespace dil {
 namespace {
 
-// Heads of an item, a power of two up to 8, or 16: what a decode kernel is made for.
-int decode_heads(int G) { return G <= 2 ? G : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
-long long decode_items(int T, int Hkv, int G) {
-  const int heads = decode_heads(G);
-  return (long long)T * Hkv * ((G + heads - 1) / heads);
+// Columns of an item: a power of two up to 8, or 16; what a decode kernel is made for. `grouped`:
+// its columns are the heads of several tokens.
+int decode_heads(int G, bool grouped) {
+  if (grouped) return G <= 4 ? 8 : 16;
+  return G <= 2 ? G : G <= 4 ? 4 : G <= 8 ? 8 : 16;
 }
-int decode_blocks_per_sm(int G, int d) { return G > 8 ? 2 : d == 64 ? 4 : 3; }
+int decode_tokens(int G, bool grouped) { return grouped ? decode_heads(G, true) / G : 1; }
+int decode_columns(int G, bool grouped) { return std::min(G * decode_tokens(G, grouped), decode_heads(G, grouped)); }
+long long decode_items(int T, int Hkv, int G, bool grouped) {
+  const int heads = decode_heads(G, grouped), tokens = decode_tokens(G, grouped);
+  return ((long long)T + tokens - 1) / tokens * Hkv * (grouped ? 1 : (G + heads - 1) / heads);
+}
+int decode_blocks_per_sm(int heads, int d) { return heads > 8 ? 2 : d == 64 ? 4 : 3; }
 
 // Blocks of a team for `items` items of up to `tiles` tiles (see decode_team_kernel), or -1: they
 // are too many or too long, and ranges of all items' tiles serve better. Up to eight tiles are
@@ -1332,17 +1338,17 @@ struct DecodeScratch {
   size_t head, walk, upto, sums, range, part;
   size_t total() const { return head + walk + upto + sums + range + part; }
 };
-DecodeScratch decode_scratch(int T, int H, int Hkv, int d) {
+DecodeScratch decode_scratch(int T, int H, int Hkv, int d, bool grouped) {
   const int G = H / Hkv;
-  const size_t items = (size_t)decode_items(T, Hkv, G);
-  const size_t warps = (size_t)kDecMaxSms * decode_blocks_per_sm(G, d) * kDecWarps;
+  const size_t items = (size_t)decode_items(T, Hkv, G, grouped);
+  const size_t warps = (size_t)kDecMaxSms * decode_blocks_per_sm(decode_heads(G, grouped), d) * kDecWarps;
   DecodeScratch s;
   s.head = align256(items * sizeof(DecodeHead));
   s.walk = align256(items * kMaxPat * sizeof(DecodeWalk));
   s.upto = align256(items * 8);
   s.sums = align256((size_t)kPlanBlocks * kPlanThreads * 8);
   s.range = align256((warps + 1) * sizeof(DecodeRange));
-  s.part = align256(warps * 2 * std::min(G, decode_heads(G)) * (d + 4) * 4);
+  s.part = align256(warps * 2 * decode_columns(G, grouped) * (d + 4) * 4);
   return s;
 }
 
@@ -1370,8 +1376,10 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
             : launch_overlapped(decode_plan_kernel<kPlanBlocks>, dim3(kPlanBlocks), kPlanThreads, 0, stream,
                                 kPlanBlocks, p);
   if (e != cudaSuccess) return e;
-  e = launch_overlapped(decode_kernel<D, HEADS, FMT>, dim3((unsigned)(p.warps / kDecWarps)),
-                        kDecWarps * 32, 0, stream, 1, p);
+  auto kernel = decode_kernel<D, HEADS, FMT, false>;
+  if constexpr (HEADS >= 8)
+    if (p.tokens > 1) kernel = decode_kernel<D, HEADS, FMT, true>;
+  e = launch_overlapped(kernel, dim3((unsigned)(p.warps / kDecWarps)), kDecWarps * 32, 0, stream, 1, p);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(p.join_items ? p.items : (p.warps + kJoinWarps - 1) / kJoinWarps),
                   (unsigned)p.part_heads);
@@ -1424,7 +1432,8 @@ void decode_patterns(DecodeParams& p, const int* w, const int* r, int npat) {
 
 extern "C" size_t dilattn_decode_workspace_size(int T, int H, int Hkv, int d) {
   if (T < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
-  return decode_scratch(T, H, Hkv, d).total();
+  const size_t plain = decode_scratch(T, H, Hkv, d, false).total();
+  return T > 1 && H / Hkv <= 8 ? std::max(plain, decode_scratch(T, H, Hkv, d, true).total()) : plain;
 }
 
 extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc, const void* vc,
@@ -1485,19 +1494,38 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   p.qk_scale = (float)(1.4426950408889634 / std::sqrt((double)d));
   decode_patterns(p, w, r, npat);
   p.G = H / Hkv;
-  p.heads = decode_heads(p.G);
-  p.nsub = (p.G + p.heads - 1) / p.heads;
+  // the most tiles that an item of one token can have, as far as the table goes
+  const long long longest = (long long)max_pages * page_size;
+  double tiles = 0;
+  for (int i = 0; i < npat; ++i) {
+    const long long n = (std::min<long long>(w[i], longest) + r[i] - 1) / r[i];
+    tiles += (double)((n + kDecTile - 1) / kDecTile);
+  }
+  p.team = decode_team((int)decode_items(T, Hkv, p.G, false), tiles, d, decode_heads(p.G, false));
+  // more tokens than sequences: several of a sequence, which dense attention takes together
+  // (while the weights of eight contexts fit an int)
+  const bool grouped =
+      p.team < 0 && p.dense && seq != nullptr && T > B && p.G <= 8 && longest < (1ll << 28);
+  p.tokens = decode_tokens(p.G, grouped);
+  p.g_rec = (256 + p.G - 1) / p.G;
+  if (grouped) {
+    tiles *= p.tokens;
+    p.npat = p.tokens;
+    for (int i = 0; i < p.npat; ++i) p.r[i] = 1;
+  }
+  p.heads = decode_heads(p.G, grouped);
+  p.nsub = grouped ? 1 : (p.G + p.heads - 1) / p.heads;
   p.per_token = Hkv * p.nsub;
   divisor_magic((uint32_t)p.per_token, p.pt_mul, p.pt_sh);
   divisor_magic((uint32_t)p.nsub, p.ns_mul, p.ns_sh);
-  p.items = (int)decode_items(T, Hkv, p.G);
+  p.items = (int)decode_items(T, Hkv, p.G, grouped);
   // the plan's cluster has room for kPlanBlocks * kPlanThreads groups: one item each while they
   // last, which it describes itself, else a block's worth each
   constexpr long long most = (long long)kPlanBlocks * kPlanThreads;
   p.group = p.items <= most ? 1 : 64 * (int)((p.items + 64 * most - 1) / (64 * most));
   p.lanes = 1;
-  while (p.lanes < npat) p.lanes *= 2;
-  const DecodeScratch lay = decode_scratch(T, H, Hkv, d);
+  while (p.lanes < p.npat) p.lanes *= 2;
+  const DecodeScratch lay = decode_scratch(T, H, Hkv, d, grouped);
   char* at = reinterpret_cast<char*>(workspace);
   auto take = [&at](size_t n) { return at += n, at - n; };
   p.head = reinterpret_cast<DecodeHead*>(take(lay.head));
@@ -1506,18 +1534,10 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   p.sums = reinterpret_cast<long long*>(take(lay.sums));
   p.range = reinterpret_cast<DecodeRange*>(take(lay.range));
   p.part = reinterpret_cast<float*>(take(lay.part));
-  p.part_heads = std::min(p.G, p.heads);
+  p.part_heads = decode_columns(p.G, grouped);
   p.part_stride = p.part_heads * (d + 4);
-  // the most tiles that an item can have, as far as the table goes
-  const long long longest = (long long)max_pages * page_size;
-  double tiles = 0;
-  for (int i = 0; i < npat; ++i) {
-    const long long n = (std::min<long long>(w[i], longest) + r[i] - 1) / r[i];
-    tiles += (double)((n + kDecTile - 1) / kDecTile);
-  }
-  p.team = decode_team(p.items, tiles, d, p.heads);
   // no more warps than have work
-  const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(p.G, d);
+  const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(p.heads, d);
   p.warps = kDecWarps * (int)std::min<double>(blocks, std::max(tiles, 1.0) * p.items * kSpreadWeight /
                                                               (kDecWarps * kRangeWeight) + 1);
   p.join_items = p.items <= p.warps / kJoinWarps;

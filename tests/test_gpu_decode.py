@@ -75,6 +75,36 @@ def test_head_layouts(H, Hkv, pats):
     check_decode(got, want, q, pair)
 
 
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 7, 8, 9])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_drafted_tokens(G, d, fmt):
+    """More tokens than sequences under dense attention: drafts in order, and tokens of any sequence
+    and position in any order, the same one twice, with empty slots between."""
+    rng = np.random.default_rng(G + d)
+    lens, Hkv = [900, 40, 3, 1, 66], 2
+    pair, table = filled(rng, lens, Hkv, 16, d, fmt, spread=3)
+    wide = np.full((len(lens), 1200), -1)  # a table for contexts that no team of blocks would be given
+    wide[:, :table.shape[1]] = table
+    drafts = [(b, n - 1 - k) for b, n in enumerate(lens) for k in range(min(n, 5) - 1, -1, -1)]
+    mixed = [(int(b), int(rng.integers(0, lens[b]))) for b in rng.integers(0, len(lens), 21)]
+    for tokens in (drafts, drafts + [(0, -1)] * 3, mixed + [(1, -1)] + mixed[:2] + [(4, -1), (0, 899)]):
+        seq, pos = [t[0] for t in tokens], [t[1] for t in tokens]
+        q = normal(rng, len(tokens), G * Hkv, d)
+        got, want = run(pair, wide, q, pos, PATS["dense"], seq)
+        check_decode(got, want, q, pair)
+    # a sequence that there is not, and a position past the table, among drafts
+    seq, pos = [0, 9, 0, 0, 1, 1], [5, 5, 2 ** 31 - 1, 7, 2, 39]
+    q = normal(rng, 6, G * Hkv, d)
+    out, lse = dilattn.decode(bf16(q).cuda(), pair.dev, i32(wide), i32(pos), PATS["dense"], seq=i32(seq))
+    torch.cuda.synchronize()
+    assert dilattn.device_error() == 4
+    ok = [0, 3, 4, 5]
+    want = ref.decode(q[ok], pair.ref, table, [pos[i] for i in ok], [seq[i] for i in ok], PATS["dense"])
+    check_decode((out[ok], lse[ok]), want, q[ok], pair)
+    assert (f64(out[1:3]) == 0).all() and torch.isneginf(lse[1:3]).all()
+
+
 def test_the_largest_patterns():
     """Segment lengths and dilations up to the largest int: each keeps one row of one head at most."""
     rng = np.random.default_rng(24)

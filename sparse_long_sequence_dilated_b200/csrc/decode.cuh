@@ -123,13 +123,12 @@ __device__ __forceinline__ bool divides(const DecodeParams& p, int i, int x) {
   return __funnelshift_r(y, y, p.r_rot[i]) <= p.r_lim[i];
 }
 
-template <int D_, int NB_>
-struct DecodeCfg {
-  static constexpr int D = D_, NB = NB_;
-  static constexpr int HEADS = 8 * NB;
-  // by registers: 128, 168 or 255 a thread; what does not fit would be loads under way
-  static constexpr int BLOCKS_PER_SM = NB == 2 ? 2 : D == 64 ? 4 : 3;
-};
+// Blocks of the main kernel on an SM, by registers: 128, 168 or 255 a thread. What
+// does not fit is loads under way, and a spill of one waits for it: eight columns
+// of drafts at d = 128 take 130 us with two blocks and 212 us with three.
+constexpr int decode_blocks_per_sm(int d, int heads, bool grouped) {
+  return heads > 8 || (d == 128 && grouped) ? 2 : d == 64 ? 4 : 3;
+}
 
 // Where an item belongs; nh: its columns. `tokens` is p.tokens, or 1 where that is known.
 struct DecodeItem {
@@ -1000,7 +999,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
 }
 
 template <int D, int HEADS, int FMT, bool GROUPED>
-__global__ void __launch_bounds__(kDecWarps * 32, (DecodeCfg<D, (HEADS + 7) / 8>::BLOCKS_PER_SM))
+__global__ void __launch_bounds__(kDecWarps * 32, decode_blocks_per_sm(D, HEADS, GROUPED))
     decode_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ uint2 s_q[kDecWarps][(HEADS + 7) / 8 * D / 16 * 32];
   __shared__ DecodeWalk s_walk[kDecWarps][kMaxPat];

@@ -1317,7 +1317,6 @@ long long decode_items(int T, int Hkv, int G, bool grouped) {
   const int heads = decode_heads(G, grouped), tokens = decode_tokens(G, grouped);
   return ((long long)T + tokens - 1) / tokens * Hkv * (grouped ? 1 : (G + heads - 1) / heads);
 }
-int decode_blocks_per_sm(int heads, int d) { return heads > 8 ? 2 : d == 64 ? 4 : 3; }
 
 // Blocks of a team for `items` items of up to `tiles` tiles (see decode_team_kernel), or -1: they
 // are too many or too long, and ranges of all items' tiles serve better. Up to eight tiles are
@@ -1341,7 +1340,7 @@ struct DecodeScratch {
 DecodeScratch decode_scratch(int T, int H, int Hkv, int d, bool grouped) {
   const int G = H / Hkv;
   const size_t items = (size_t)decode_items(T, Hkv, G, grouped);
-  const size_t warps = (size_t)kDecMaxSms * decode_blocks_per_sm(decode_heads(G, grouped), d) * kDecWarps;
+  const size_t warps = (size_t)kDecMaxSms * decode_blocks_per_sm(d, decode_heads(G, grouped), grouped) * kDecWarps;
   DecodeScratch s;
   s.head = align256(items * sizeof(DecodeHead));
   s.walk = align256(items * kMaxPat * sizeof(DecodeWalk));
@@ -1537,7 +1536,7 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   p.part_heads = decode_columns(p.G, grouped);
   p.part_stride = p.part_heads * (d + 4);
   // no more warps than have work
-  const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(p.heads, d);
+  const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(d, p.heads, grouped);
   p.warps = kDecWarps * (int)std::min<double>(blocks, std::max(tiles, 1.0) * p.items * kSpreadWeight /
                                                               (kDecWarps * kRangeWeight) + 1);
   p.join_items = p.items <= p.warps / kJoinWarps;

@@ -23,14 +23,14 @@
 // ranges of equal weight, one for each warp of a persistent grid, wherever the cut
 // falls: no batch shape, length or head count leaves SMs idle. Warps do not
 // wait for one another. An item inside one range is finished by its warp; an
-// item that is cut leaves partials that decode_join_kernel combines in warp
+// item that is cut leaves partials that a join kernel combines in warp
 // order (no atomics: the same call gives the same bits).
 //
 // Launches: few or short items have decode_team_kernel alone. Otherwise
 // decode_plan_kernel, one block or cluster, describes every item's walks once
 // and cuts the sequence (above kPlanBlocks * kPlanThreads items,
 // decode_walks_kernel describes them before it, over the whole GPU), then
-// decode_kernel, then decode_join_kernel. Each is launched while the one before
+// decode_kernel, then a join kernel. Each is launched while the one before
 // it runs and waits for that one's end.
 #pragma once
 
@@ -93,7 +93,6 @@ struct DecodeParams {
   int lanes;                 // threads that describe an item: a power of two, at least npat
   int warps;                 // warps of the grid
   int team;                  // blocks that share an item in decode_team_kernel; 0: a warp for each item
-  int join_items;            // decode_join_kernel has a block for each item, not for every 8 ranges
   float qk_scale;            // log2(e) / sqrt(d)
   int npat;                  // patterns, by ascending r
   int dense;                 // one pattern with r = 1: every head of a token takes every row of a walk
@@ -1135,172 +1134,222 @@ __global__ void __launch_bounds__(kTeamWarps * 32, D == 64 && HEADS <= 8 ? 2 : 1
 
 // ---------------------------------------------------------------------------
 // Join of cut items. An item that begins in warp w's range and goes on past it
-// has its partials in slot 1 of w and in slot 0 of the warps behind it. A block
-// has the items that begin in kJoinWarps successive ranges, and one head of
-// them. An item of up to 32 partials is one warp's; longer ones (at most one
-// begins within so few ranges) are the whole block's. Fewer items than there
-// would be blocks have a block each (p.join_items).
+// has its partials in slot 1 of w and in slot 0 of the warps behind it.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
 constexpr int kJoinPart = 512;  // partials whose weights are held at a time
+constexpr int kJoinShort = 32;  // most partials that one warp joins
 
+// The partials of an item: the k-th one from range w on.
+struct JoinParts {
+  const float* first;
+  const float* rest;  // partial k > 0 at rest + k step
+  size_t step;
+  __device__ JoinParts(const DecodeParams& p, int w)
+      : first(p.part + ((size_t)w * 2 + 1) * p.part_stride),
+        rest(p.part + (size_t)w * 2 * p.part_stride),
+        step((size_t)2 * p.part_stride) {}
+  __device__ const float* operator()(int k) const { return k == 0 ? first : rest + k * step; }
+};
+
+// One warp joins a column of up to kJoinShort partials.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads, 4) decode_join_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int LANES = D / 4, ROWS = 32 / LANES;  // threads of a row, rows that a warp reads at a time
+__device__ __forceinline__ void join_short(const DecodeParams& p, const DecodeItem& it, int w, int n, int column) {
+  constexpr int LANES = D / 4, ROWS = 32 / LANES;  // threads of a row, rows at a time
   constexpr int EAGER = 4;
-  __shared__ float s_l[kJoinPart], s_v[kJoinPart];
-  __shared__ float s_red[kJoinWarps][2];
-  __shared__ float4 s_acc[kJoinThreads / LANES][LANES];
-  __shared__ int s_long;        // range in which an item of more than 32 partials begins
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hl = blockIdx.y;
-  const size_t step = (size_t)2 * p.part_stride;
-  const int so = p.part_heads * D + hl * 4;
-  int w = -1, n = 0;            // range in which the block's item begins, and its partials
-  // The ranges are there: this kernel was let start after every block of the main one had waited
-  // for the plan. What other kernels left of them in L1 is passed over.
-  auto range = [&](int k) {
-    const int2 x = __ldcg(reinterpret_cast<const int2*>(p.range + k));
-    return DecodeRange{x.x, x.y};
-  };
-  if (p.join_items) {
-    const int item = (int)blockIdx.x;
-    int before = 0, in = 0;     // ranges that begin up to the item's beginning, and inside it
-    for (int k = tid; k <= p.warps; k += kJoinThreads) {
-      const DecodeRange r = range(k);
-      before += r.item < item || (r.item == item && r.tile == 0);
-      in += r.item == item && r.tile > 0;
-    }
-    before = __reduce_add_sync(0xffffffffu, before);
-    in = __reduce_add_sync(0xffffffffu, in);
-    if (lane == 0) s_red[warp][0] = __int_as_float(before), s_red[warp][1] = __int_as_float(in);
-    __syncthreads();
-    before = in = 0;
+  const int lane = threadIdx.x & 31, row = lane / LANES, col = lane % LANES;
+  const JoinParts part(p, w);
+  float4 st = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+  if (lane < n) st = *reinterpret_cast<const float4*>(part(lane) + p.part_heads * D + column * 4);
+  float4 x[EAGER];  // the first rows come along with the statistics
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) before += __float_as_int(s_red[k][0]), in += __float_as_int(s_red[k][1]);
-    __syncthreads();
-    grid_dependency_wait();
-    grid_dependency_release();
-    if (in == 0) return;
-    w = before - 1;
-    n = in + 1;
-  } else {
-    if (tid == 0) s_long = -1;
-    const int w_own = (int)blockIdx.x * kJoinWarps + warp;
-    DecodeRange a{0, 0}, b{0, 0}, r{-1, 0};  // r: ranges w_own + 1 .., those that hold a part of the item
-    if (w_own < p.warps) {
-      a = range(w_own);
-      b = range(w_own + 1);
-      if (w_own + 1 + lane < p.warps) r = range(w_own + 1 + lane);
-    }
-    grid_dependency_wait();
-    grid_dependency_release();
-    __syncthreads();
-    w = w_own;
-    const DecodeItem it = item_of(p, b.tile > 0 ? b.item : 0, p.tokens);
-    // an item begins in range w and goes on past it
-    if (b.tile > 0 && (a.item != b.item || a.tile == 0) && hl < it.nh) {
-      const uint32_t held = __ballot_sync(0xffffffffu, r.item == b.item);
-      if (held == 0xffffffffu) {
-        if (lane == 0) s_long = w;
-      } else {
-        const int n = __popc(held) + 1;
-        const float* first = p.part + ((size_t)w * 2 + 1) * p.part_stride;
-        const float* rest = p.part + (size_t)(w + 1) * 2 * p.part_stride - step;  // partial k at rest + k step
-        const int row = lane / LANES, col = lane % LANES;
-        float4 st = make_float4(kNoMax, kNoMax, 0.f, 0.f);
-        if (lane < n) st = *reinterpret_cast<const float4*>((lane == 0 ? first : rest + lane * step) + so);
-        float4 x[EAGER];  // the first rows come along with the statistics
-#pragma unroll
-        for (int i = 0; i < EAGER; ++i) {
-          const int k = i * ROWS + row;
-          if (k < n) x[i] = *reinterpret_cast<const float4*>((k == 0 ? first : rest + k * step) + hl * D + col * 4);
-        }
-        const float M = warp_max(st.x), MV = warp_max(st.y);
-        const float L = warp_sum(lane < n ? st.z * exp2f(st.x - M) : 0.f);
-        const float f = exp2f(st.y - MV);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < EAGER; ++i) {
-          const float fk = __shfl_sync(0xffffffffu, f, i * ROWS + row);
-          if (i * ROWS + row < n) add_scaled(acc, x[i], fk);
-        }
-#pragma unroll 8
-        for (int k0 = EAGER * ROWS; k0 < n; k0 += ROWS) {
-          const int k = k0 + row;
-          const float fk = __shfl_sync(0xffffffffu, f, k & 31);
-          if (k < n) add_scaled(acc, *reinterpret_cast<const float4*>(rest + k * step + hl * D + col * 4), fk);
-        }
-        if constexpr (LANES == 16) {
-          acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
-          acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
-          acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
-          acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
-        }
-        if (row == 0) store_joined(p, D, place_of(p, it, hl, p.tokens), col, acc, M, MV, L);
-      }
-    }
-    __syncthreads();
-    w = s_long;
-    if (w < 0) return;
-    const int item = range(w + 1).item;
-    for (int k = w + 1 + tid;; k += kJoinThreads) {
-      const int got = __syncthreads_count(k < p.warps && range(k).item == item);
-      n += got;
-      if (got < kJoinThreads) break;
-    }
-    ++n;
+  for (int i = 0; i < EAGER; ++i) {
+    const int k = i * ROWS + row;
+    if (k < n) x[i] = *reinterpret_cast<const float4*>(part(k) + column * D + col * 4);
   }
-  const DecodeItem it = item_of(p, p.join_items ? (int)blockIdx.x : range(w + 1).item, p.tokens);
-  if (hl >= it.nh) return;
-  const float* first = p.part + ((size_t)w * 2 + 1) * p.part_stride;
-  const float* rest = p.part + (size_t)(w + 1) * 2 * p.part_stride - step;
-  // the largest maxima
+  const float M = warp_max(st.x), MV = warp_max(st.y);
+  const float L = warp_sum(lane < n ? st.z * exp2f(st.x - M) : 0.f);
+  const float f = exp2f(st.y - MV);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < EAGER; ++i) {
+    const float fk = __shfl_sync(0xffffffffu, f, i * ROWS + row);
+    if (i * ROWS + row < n) add_scaled(acc, x[i], fk);
+  }
+#pragma unroll 4
+  for (int k0 = EAGER * ROWS; k0 < n; k0 += ROWS) {
+    const int k = k0 + row;
+    const float fk = __shfl_sync(0xffffffffu, f, k & 31);
+    if (k < n) add_scaled(acc, *reinterpret_cast<const float4*>(part(k) + column * D + col * 4), fk);
+  }
+  if constexpr (LANES == 16) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+  }
+  if (row == 0) store_joined(p, D, place_of(p, it, column, p.tokens), col, acc, M, MV, L);
+}
+
+// A block joins a column of any number of partials; BATCH: rows of a thread under way at once.
+template <int D, int BATCH>
+__device__ __forceinline__ void join_long(const DecodeParams& p, const DecodeItem& it, int w, int n, int column) {
+  constexpr int LANES = D / 4, STEP = kJoinThreads / LANES;
+  constexpr int OWN = kJoinPart / kJoinThreads;
+  __shared__ float s_l[kJoinPart], s_v[kJoinPart];
+  __shared__ float s_top[kJoinWarps][2], s_sum;
+  __shared__ float4 s_acc[STEP][LANES];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = tid / LANES, col = tid % LANES;
+  const int so = p.part_heads * D + column * 4;
+  const JoinParts part(p, w);
+  // statistics of the first kJoinPart partials, and the first rows of sums, come along
+  float4 st[OWN], x[BATCH];
+  auto load_rows = [&](int base, int i0, int cnt) {
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int i = i0 + j * STEP;
+      if (i < cnt) x[j] = *reinterpret_cast<const float4*>(part(base + i) + column * D + col * 4);
+    }
+  };
   float2 top = make_float2(kNoMax, kNoMax);
-  for (int k = tid; k < n; k += kJoinThreads) {
-    const float2 f = *reinterpret_cast<const float2*>((k == 0 ? first : rest + k * step) + so);
-    top.x = fmaxf(top.x, f.x);
-    top.y = fmaxf(top.y, f.y);
+#pragma unroll
+  for (int u = 0; u < OWN; ++u) {
+    const int k = tid + u * kJoinThreads;
+    st[u] = k < n ? *reinterpret_cast<const float4*>(part(k) + so) : make_float4(kNoMax, kNoMax, 0.f, 0.f);
+  }
+  load_rows(0, row, min(n, kJoinPart));
+#pragma unroll
+  for (int u = 0; u < OWN; ++u) top = make_float2(fmaxf(top.x, st[u].x), fmaxf(top.y, st[u].y));
+  for (int k = kJoinPart + tid; k < n; k += kJoinThreads) {
+    const float2 f = *reinterpret_cast<const float2*>(part(k) + so);
+    top = make_float2(fmaxf(top.x, f.x), fmaxf(top.y, f.y));
   }
   float M = warp_max(top.x), MV = warp_max(top.y);
-  if (lane == 0) s_red[warp][0] = M, s_red[warp][1] = MV;
+  if (lane == 0) s_top[warp][0] = M, s_top[warp][1] = MV;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kJoinWarps; ++k) {
-    M = fmaxf(M, s_red[k][0]);
-    MV = fmaxf(MV, s_red[k][1]);
+    M = fmaxf(M, s_top[k][0]);
+    MV = fmaxf(MV, s_top[k][1]);
   }
   // sums, in the partials' order
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int row = tid / LANES, col = tid % LANES;
   for (int base = 0; base < n; base += kJoinPart) {
     const int cnt = min(kJoinPart, n - base);
-    for (int i = tid; i < cnt; i += kJoinThreads) {
-      const int k = base + i;
-      const float4 f = *reinterpret_cast<const float4*>((k == 0 ? first : rest + k * step) + so);
-      s_l[i] = f.z * exp2f(f.x - M);
-      s_v[i] = exp2f(f.y - MV);
+#pragma unroll
+    for (int u = 0; u < OWN; ++u) {
+      const int i = tid + u * kJoinThreads;
+      if (base > 0 && i < cnt) st[u] = *reinterpret_cast<const float4*>(part(base + i) + so);
+      if (i < cnt) {
+        s_l[i] = st[u].z * exp2f(st[u].x - M);
+        s_v[i] = exp2f(st[u].y - MV);
+      }
     }
     __syncthreads();
-#pragma unroll 8
-    for (int i = row; i < cnt; i += kJoinThreads / LANES) {
-      const int k = base + i;
-      add_scaled(acc, *reinterpret_cast<const float4*>((k == 0 ? first : rest + k * step) + hl * D + col * 4), s_v[i]);
+    for (int i0 = row; i0 < cnt; i0 += STEP * BATCH) {
+      if (base > 0 || i0 != row) load_rows(base, i0, cnt);
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (i0 + j * STEP < cnt) add_scaled(acc, x[j], s_v[i0 + j * STEP]);
     }
     if (warp == 0)
       for (int i = lane; i < cnt; i += 32) L += s_l[i];
     __syncthreads();
   }
   s_acc[row][col] = acc;
-  L = warp_sum(L);
+  if (warp == 0) {
+    L = warp_sum(L);
+    if (lane == 0) s_sum = L;
+  }
   __syncthreads();
-  if (tid < LANES) {  // these are warp 0's threads
+  if (tid < LANES) {
     float4 a = s_acc[0][tid];
 #pragma unroll
-    for (int k = 1; k < kJoinThreads / LANES; ++k) add_scaled(a, s_acc[k][tid], 1.f);
-    store_joined(p, D, place_of(p, it, hl, p.tokens), tid, a, M, MV, L);
+    for (int k = 1; k < STEP; ++k) add_scaled(a, s_acc[k][tid], 1.f);
+    store_joined(p, D, place_of(p, it, column, p.tokens), tid, a, M, MV, s_sum);
   }
+}
+
+// The ranges are there before a join kernel waits: it was let start after every block of the main
+// one had waited for the plan. What other kernels left of them in L1 is passed over.
+__device__ __forceinline__ DecodeRange range_of(const DecodeParams& p, int k) {
+  const int2 x = __ldcg(reinterpret_cast<const int2*>(p.range + k));
+  return DecodeRange{x.x, x.y};
+}
+
+// Few items: blockIdx.x is the item, whose columns are a warp's each when it has few partials, and
+// else a block's each.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads, 2) decode_join_items_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ int s_cnt[kJoinWarps][2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, item = (int)blockIdx.x;
+  int before = 0, in = 0;  // ranges that begin up to the item's beginning, and inside it
+  for (int k = tid; k <= p.warps; k += kJoinThreads) {
+    const DecodeRange r = range_of(p, k);
+    before += r.item < item || (r.item == item && r.tile == 0);
+    in += r.item == item && r.tile > 0;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  in = __reduce_add_sync(0xffffffffu, in);
+  if (lane == 0) s_cnt[warp][0] = before, s_cnt[warp][1] = in;
+  __syncthreads();
+  before = in = 0;
+#pragma unroll
+  for (int k = 0; k < kJoinWarps; ++k) before += s_cnt[k][0], in += s_cnt[k][1];
+  grid_dependency_wait();
+  grid_dependency_release();
+  const int w = before - 1, n = in + 1;
+  if (n == 1) return;  // not cut
+  const DecodeItem it = item_of(p, item, p.tokens);
+  if (n <= kJoinShort) {
+    const int column = (int)blockIdx.y * kJoinWarps + warp;
+    if (column < it.nh) join_short<D>(p, it, w, n, column);
+  } else if ((int)blockIdx.y < it.nh) {
+    join_long<D, 8>(p, it, w, n, blockIdx.y);
+  }
+}
+
+// Many items: block (x, y) has column y of the items that begin in ranges 8 x .. 8 x + 7, a warp
+// each; one of more partials (no second one begins in eight ranges) is the whole block's.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads, 5) decode_join_ranges_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ int s_long;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, column = blockIdx.y;
+  const int w = (int)blockIdx.x * kJoinWarps + warp;
+  if (tid == 0) s_long = -1;
+  DecodeRange a{0, 0}, b{0, 0}, r{-1, 0};  // r: ranges w + 1 .., those that hold a part of the item
+  if (w < p.warps) {
+    a = range_of(p, w);
+    b = range_of(p, w + 1);
+    if (w + 1 + lane < p.warps) r = range_of(p, w + 1 + lane);
+  }
+  grid_dependency_wait();
+  grid_dependency_release();
+  __syncthreads();
+  // an item begins in range w and goes on past it
+  if (b.tile > 0 && (a.item != b.item || a.tile == 0)) {
+    const DecodeItem it = item_of(p, b.item, p.tokens);
+    const uint32_t held = __ballot_sync(0xffffffffu, r.item == b.item);
+    if (column >= it.nh) {
+    } else if (__popc(held) < kJoinShort) {
+      join_short<D>(p, it, w, __popc(held) + 1, column);
+    } else if (lane == 0) {
+      s_long = w;
+    }
+  }
+  __syncthreads();
+  const int wl = s_long;
+  if (wl < 0) return;
+  const int item = range_of(p, wl + 1).item;
+  int n = 1;
+  for (int k = wl + 1 + tid;; k += kJoinThreads) {
+    const int got = __syncthreads_count(k < p.warps && range_of(p, k).item == item);
+    n += got;
+    if (got < kJoinThreads) break;
+  }
+  join_long<D, 2>(p, item_of(p, item, p.tokens), wl, n, column);  // rare: registers for more blocks
 }
 
 }  // namespace dil

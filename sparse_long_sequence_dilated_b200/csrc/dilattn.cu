@@ -1380,9 +1380,12 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
     if (p.tokens > 1) kernel = decode_kernel<D, HEADS, FMT, true>;
   e = launch_overlapped(kernel, dim3((unsigned)(p.warps / kDecWarps)), kDecWarps * 32, 0, stream, 1, p);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(p.join_items ? p.items : (p.warps + kJoinWarps - 1) / kJoinWarps),
-                  (unsigned)p.part_heads);
-  return launch_overlapped(decode_join_kernel<D>, grid, kJoinThreads, 0, stream, 1, p);
+  // a block for each item while they are fewer than blocks for every eight ranges
+  const int by_ranges = (p.warps + kJoinWarps - 1) / kJoinWarps;
+  const bool few = p.items <= by_ranges;
+  return launch_overlapped(few ? decode_join_items_kernel<D> : decode_join_ranges_kernel<D>,
+                           dim3((unsigned)(few ? p.items : by_ranges), (unsigned)p.part_heads), kJoinThreads, 0, stream,
+                           1, p);
 }
 template <int D, int FMT>
 cudaError_t launch_decode_heads(const DecodeParams& p, cudaStream_t stream) {
@@ -1539,7 +1542,6 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(d, p.heads, grouped);
   p.warps = kDecWarps * (int)std::min<double>(blocks, std::max(tiles, 1.0) * p.items * kSpreadWeight /
                                                               (kDecWarps * kRangeWeight) + 1);
-  p.join_items = p.items <= p.warps / kJoinWarps;
   cudaError_t e;
   if (format == DILATTN_CACHE_E4M3)
     e = d == 64 ? launch_decode_heads<64, kFmtE4M3>(p, stream) : launch_decode_heads<128, kFmtE4M3>(p, stream);

@@ -153,6 +153,24 @@ def test_many_short_tokens():
         check_decode(got, want, q, pair)
 
 
+@pytest.mark.parametrize("T,H,Hkv,pats", [
+    (1400, 8, 4, "dense"),                        # a token of each of 1400 sequences
+    (1100, 8, 4, [(1000, 1), (1000, 2)]),
+    (4200, 8, 8, "dense"),                        # tokens of some of them together
+])
+def test_more_items_than_the_plan_describes_at_once(T, H, Hkv, pats):
+    rng = np.random.default_rng(25)
+    lens = list(rng.integers(1, 30, 1399)) + [700]  # the long one keeps the table wide
+    pair, table = filled(rng, lens, Hkv, 16, 64, "int8")
+    seq = np.arange(T) if T <= len(lens) else np.sort(rng.integers(0, len(lens), T))
+    pos = np.array([rng.integers(-1, lens[s]) for s in seq])
+    pos[-1] = lens[seq[-1]] - 1
+    q = normal(rng, T, H, 64)
+    pats = PATS["dense"] if pats == "dense" else pats
+    got, want = run(pair, table, q, pos, pats, seq)
+    check_decode(got, want, q, pair)
+
+
 def test_sharp_and_flat_softmax():
     """Queries whose scores differ by hundreds, and zero queries (the mean of the rows)."""
     rng = np.random.default_rng(13)

@@ -129,6 +129,11 @@ constexpr int decode_blocks_per_sm(int d, int heads, bool grouped) {
   return heads > 8 || (d == 128 && grouped) ? 2 : d == 64 ? 4 : 3;
 }
 
+// What a kernel is made for: any patterns (dense ones too), one dense pattern and
+// a token to an item (which spares the counting of patterns for every score), and
+// one dense pattern and several tokens to an item.
+enum DecodeMode : int { kAnyPatterns = 0, kDense = 1, kGrouped = 2 };
+
 // Where an item belongs; nh: its columns. `tokens` is p.tokens, or 1 where that is known.
 struct DecodeItem {
   int token, hk, h0, nh;
@@ -503,8 +508,7 @@ __device__ __forceinline__ float final_lse(float m, float l) {
 // walk[0] from item first_item on; part: the warp's two slots for partials, slot_stride
 // floats apart; qf, s_walk: shared memory of the warp (the lane's own fragments
 // of Q, NB * MT of them 32 apart, and the walks of the item to fetch from).
-// GROUPED: p.tokens > 1.
-template <int D, int HEADS, int FMT, bool GROUPED>
+template <int D, int HEADS, int FMT, int MODE>
 __device__ __forceinline__ void decode_range(const DecodeParams& p, const DecodeRange rg, const DecodeRange end,
                                              const DecodeHead* head, const DecodeWalk* walk, int first_item,
                                              float* part, size_t slot_stride, uint2* qf, DecodeWalk* s_walk) {
@@ -513,6 +517,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
   constexpr int HW = HEADS < 8 ? HEADS : 8;        // heads of an MMA's columns
   constexpr int VR = HW <= 2 ? 1 : HW / 2;         // rows of a tile that a lane's softmax has
   constexpr int VE = HW == 1 ? 1 : 2;              // heads of them, for each NB
+  constexpr bool GROUPED = MODE == kGrouped;
   const int tokens_of_item = GROUPED ? p.tokens : 1;
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -568,7 +573,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
       f_x = x0 + row_l * a_r;
       f_page = p.geom.table[(size_t)a_b * p.geom.max_pages + (f_x >> p.geom.lp)];
     }
-    if (GROUPED || p.dense) {
+    if (MODE != kAnyPatterns || p.dense) {
       f_meta = k < n ? (GROUPED ? (uint32_t)f_x + 1 : 1u) : 0u;
     } else {
       // patterns that hold the row: low half; the one that walks it and all before: high half
@@ -617,8 +622,11 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
       in = false;
     }
     const uint32_t blk = in ? (uint32_t)f_page * (uint32_t)p.geom.Hkv + (uint32_t)f_hk : 0u;
-    ks_l = p.scale[0][blk];
-    vs_l = p.scale[1][blk];
+    ks_l = vs_l = 1.f;
+    if (in) {
+      ks_l = p.scale[0][blk];
+      vs_l = p.scale[1][blk];
+    }
     meta_l = in ? f_meta : 0u;
     walk_l = f_j;
     row = in ? (blk << p.geom.lp) + (uint32_t)(f_x & pmask) : 0u;
@@ -858,7 +866,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
           ks[v] = __shfl_sync(0xffffffffu, ks_l, from);
           lv[v] = __shfl_sync(0xffffffffu, lv_l, from);
         }
-        if (VR > 1 && (GROUPED || !(whole && p.dense))) meta[v] = __shfl_sync(0xffffffffu, meta_l, from);
+        if (VR > 1 && (GROUPED || !(whole && (MODE == kDense || p.dense)))) meta[v] = __shfl_sync(0xffffffffu, meta_l, from);
       }
     }
     more = f_some;
@@ -887,19 +895,26 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
           } else {
             x = sc[v >> 1][nb][(v & 1) * 2 + e];
           }
-          bool ok = meta[v] != 0;
+          float s, t;
           cnt[v][nb][e] = 1.f;
-          if constexpr (HEADS == 1) {
-            cnt[v][nb][e] = (float)(meta[v] & 31u);
-          } else if (p.dense) {
-            if constexpr (GROUPED) ok = ok && (int)(meta[v] - 1) <= upto_pos[i] && (in_pat[i] >> walk_j & 1u);
+          if constexpr (MODE == kDense) {
+            // a row that is not there has -infinity for its bias and finite codes and scales
+            s = fmaf(x, fac[i] * ks[v], meta[v] != 0 ? 0.f : -INFINITY);
+            t = s + lv[v];
           } else {
-            const uint32_t u = meta[v] & in_pat[i], upto = meta[v] >> 16;
-            ok = ok && (u & upto) == (upto ^ (upto >> 1));
-            cnt[v][nb][e] = (float)__popc(u);
+            bool ok = meta[v] != 0;
+            if constexpr (GROUPED) {
+              ok = ok && (int)(meta[v] - 1) <= upto_pos[i] && (in_pat[i] >> walk_j & 1u);
+            } else if constexpr (HEADS == 1) {
+              cnt[v][nb][e] = (float)(meta[v] & 31u);
+            } else if (!p.dense) {
+              const uint32_t u = meta[v] & in_pat[i], upto = meta[v] >> 16;
+              ok = ok && (u & upto) == (upto ^ (upto >> 1));
+              cnt[v][nb][e] = (float)__popc(u);
+            }
+            s = ok ? x * (fac[i] * ks[v]) : -INFINITY;
+            t = ok ? s + lv[v] : -INFINITY;
           }
-          const float s = ok ? x * (fac[i] * ks[v]) : -INFINITY;
-          const float t = ok ? s + lv[v] : -INFINITY;
           s1[v][nb][e] = s;
           s2[v][nb][e] = t;
           raise = raise || s > m[i] + kMaxSlack || t > mv[i] + kMaxSlack;
@@ -945,8 +960,9 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           const int i = 2 * nb + e;
-          l[i] += fast_exp2(s1[v][nb][e] - m[i]) * cnt[v][nb][e];
-          pv[e] = fast_exp2(s2[v][nb][e] - (mv[i] - kPBias)) * cnt[v][nb][e];
+          const float p1 = fast_exp2(s1[v][nb][e] - m[i]), p2 = fast_exp2(s2[v][nb][e] - (mv[i] - kPBias));
+          l[i] += MODE == kAnyPatterns ? p1 * cnt[v][nb][e] : p1;
+          pv[e] = MODE == kAnyPatterns ? p2 * cnt[v][nb][e] : p2;
         }
         const __half2 h2 = __floats2half2_rn(pv[0], pv[1]);
         tr[v] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h2));
@@ -997,8 +1013,8 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
   }
 }
 
-template <int D, int HEADS, int FMT, bool GROUPED>
-__global__ void __launch_bounds__(kDecWarps * 32, decode_blocks_per_sm(D, HEADS, GROUPED))
+template <int D, int HEADS, int FMT, int MODE>
+__global__ void __launch_bounds__(kDecWarps * 32, decode_blocks_per_sm(D, HEADS, MODE == kGrouped))
     decode_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ uint2 s_q[kDecWarps][(HEADS + 7) / 8 * D / 16 * 32];
   __shared__ DecodeWalk s_walk[kDecWarps][kMaxPat];
@@ -1009,7 +1025,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, decode_blocks_per_sm(D, HEADS,
   const DecodeRange rg = p.range[wi], end = p.range[wi + 1];
   grid_dependency_release();
   if (rg.item == end.item && rg.tile == end.tile) return;
-  decode_range<D, HEADS, FMT, GROUPED>(p, rg, end, p.head, p.walk, 0, p.part + (size_t)wi * 2 * p.part_stride,
+  decode_range<D, HEADS, FMT, MODE>(p, rg, end, p.head, p.walk, 0, p.part + (size_t)wi * 2 * p.part_stride,
                                        p.part_stride, s_q[warp] + lane, s_walk[warp]);
 }
 
@@ -1079,7 +1095,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32, D == 64 && HEADS <= 8 ? 2 : 1
     }
     float* const part = s_part + warp * p.part_stride;
     if (alone || rg.tile < end.tile)
-      decode_range<D, HEADS, FMT, false>(p, rg, end, &s_head[own], s_desc[own], item, part, 0, s_q[warp] + lane,
+      decode_range<D, HEADS, FMT, kAnyPatterns>(p, rg, end, &s_head[own], s_desc[own], item, part, 0, s_q[warp] + lane,
                                          s_walk[warp]);
     else if (lane < p.part_heads)
       reinterpret_cast<float4*>(part + stat)[lane] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
@@ -1314,7 +1330,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) decode_join_items_kernel(cons
 // Many items: block (x, y) has column y of the items that begin in ranges 8 x .. 8 x + 7, a warp
 // each; one of more partials (no second one begins in eight ranges) is the whole block's.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads, 5) decode_join_ranges_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kJoinThreads, 4) decode_join_ranges_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ int s_long;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, column = blockIdx.y;
   const int w = (int)blockIdx.x * kJoinWarps + warp;

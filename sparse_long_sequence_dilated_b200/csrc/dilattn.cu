@@ -1375,9 +1375,9 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
             : launch_overlapped(decode_plan_kernel<kPlanBlocks>, dim3(kPlanBlocks), kPlanThreads, 0, stream,
                                 kPlanBlocks, p);
   if (e != cudaSuccess) return e;
-  auto kernel = decode_kernel<D, HEADS, FMT, false>;
+  auto kernel = p.dense ? decode_kernel<D, HEADS, FMT, kDense> : decode_kernel<D, HEADS, FMT, kAnyPatterns>;
   if constexpr (HEADS >= 8)
-    if (p.tokens > 1) kernel = decode_kernel<D, HEADS, FMT, true>;
+    if (p.tokens > 1) kernel = decode_kernel<D, HEADS, FMT, kGrouped>;
   e = launch_overlapped(kernel, dim3((unsigned)(p.warps / kDecWarps)), kDecWarps * 32, 0, stream, 1, p);
   if (e != cudaSuccess) return e;
   // a block for each item while they are fewer than blocks for every eight ranges

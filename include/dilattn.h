@@ -304,8 +304,15 @@ int dilattn_cache_read(const void* kc, const void* vc, const float* ks, const fl
  * lse [T][H] float32, natural log, or NULL. pos[i] < 0 is an empty slot: like
  * a token that no pattern keeps it gets out = 0 and lse = -inf.
  *
- * Scores, softmax and sums are fp32; q and the codes are exact operands, and
- * the probabilities are rounded to 11 bits for the product with V.
+ * Tokens may come in any order and share a sequence (drafted tokens: with a
+ * pattern of r = 1 that holds every position, tokens of one sequence that
+ * follow one another in q read the cache together).
+ *
+ * Scores, softmax and sums are fp32; q (elements below 2^-37 of its head's
+ * largest aside) and the codes are exact operands, and the probabilities are
+ * rounded to 11 bits for the product with V. The same call on the same inputs
+ * gives the same bits; a token's bits may depend on the other tokens of its
+ * call, whose number decides how sums are split.
  *
  * workspace: at least dilattn_decode_workspace_size(T, H, Hkv, d) bytes,
  * 256-byte aligned; its contents on entry do not matter. Calls that can

@@ -93,6 +93,12 @@ def test_drafted_tokens(G, d, fmt):
         q = normal(rng, len(tokens), G * Hkv, d)
         got, want = run(pair, wide, q, pos, PATS["dense"], seq)
         check_decode(got, want, q, pair)
+    # segments end inside the sequences: tokens of one need not share rows
+    seq, pos = [t[0] for t in drafts] * 8, [t[1] for t in drafts] * 8
+    q = normal(rng, len(seq), G * Hkv, d)
+    for w in (600, 64, 3):
+        got, want = run(pair, wide, q, pos, [(w, 1)], seq)
+        check_decode(got, want, q, pair)
     # a sequence that there is not, and a position past the table, among drafts
     seq, pos = [0, 9, 0, 0, 1, 1], [5, 5, 2 ** 31 - 1, 7, 2, 39]
     q = normal(rng, 6, G * Hkv, d)

@@ -1359,9 +1359,11 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   if (p.team >= 0) {
     const auto kernel = decode_team_kernel<D, HEADS, FMT>;
     const size_t smem = p.team == 0 ? 0 : (size_t)(kTeamWarps + 1) * p.part_stride * 4;
-    // with the static part more than 48 KB; opting in is needed once per device and costs nothing to repeat
+    // with the static part more than 48 KB; opting in (always to the same most, for calls of other
+    // threads) is needed once per device and costs nothing to repeat
     if constexpr (HEADS * D >= 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (kTeamWarps + 1) * HEADS * (D + 4) * 4);
       if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)(p.team == 0 ? (p.items + kTeamWarps - 1) / kTeamWarps : p.items * p.team));

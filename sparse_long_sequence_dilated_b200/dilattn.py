@@ -563,7 +563,7 @@ def decode_workspace_size(T: int, H: int, Hkv: int, d: int) -> int:
 
 
 def decode_workspace(T: int, H: int, Hkv: int, d: int, device="cuda"):
-    """A workspace for decode calls of up to these sizes. Calls that can overlap on the GPU
+    """A workspace for decode calls of up to T tokens with these heads. Calls that can overlap on the GPU
     (other streams, graphs that replay at the same time) need one each."""
     torch = _torch()
     return torch.empty(max(decode_workspace_size(T, H, Hkv, d), 256), dtype=torch.uint8,

@@ -577,7 +577,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
     f_page = -1;
     f_meta = 0;
     const int x0 = (int)((uint32_t)a_base + a_k * (uint32_t)a_r);
-    f_whole = a_r == 1 && a_k + kDecTile <= n && (x0 & pmask) + kDecTile <= pmask + 1;
+    f_whole = a_r == 1 && a_k + kDecTile <= n && (x0 & 15) == 0;  // no page ends inside a half
     if (k < n) {
       f_x = x0 + row_l * a_r;
       f_page = p.geom.table[(size_t)a_b * p.geom.max_pages + (f_x >> p.geom.lp)];
@@ -617,7 +617,7 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
   constexpr int KQ = D / 64, VW = D / 32;  // 16-byte pieces of a K row, words of a V row, that a lane holds
   const uint8_t* const base_k = p.codes[0] + c * 16;
   const uint8_t* const base_v = p.codes[1] + g * (D / 8);
-  uint32_t row = 0, meta_l = 0;  // this lane's row of the cache, and what f_meta said of it
+  uint32_t row = 0, row2 = 0, meta_l = 0;  // this lane's row of the cache, and what f_meta said of it
   float ks_l = 0.f, vs_l = 0.f;
   int walk_l = 0;
   bool whole = false, any = false;
@@ -642,18 +642,22 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
     const uint32_t ins = __ballot_sync(0xffffffffu, in);
     any = ins != 0;
     whole = f_whole && ins == 0xffffffffu;
-    // a row that does not count stands for one that does: its codes are finite
-    const uint32_t other = __shfl_sync(0xffffffffu, row, any ? __ffs(ins) - 1 : 0);
-    if (whole) row -= (uint32_t)row_l;  // the tile's first row
-    else if (!in) row = other;
+    if (whole) {  // two stretches of 16 rows: their first rows are lane 0's and, in slot 2, lane 2's
+      row2 = __shfl_sync(0xffffffffu, row, 2);
+      row = __shfl_sync(0xffffffffu, row, 0);
+    } else {
+      // a row that does not count stands for one that does: its codes are finite
+      const uint32_t other = __shfl_sync(0xffffffffu, row, any ? __ffs(ins) - 1 : 0);
+      if (!in) row = other;
+    }
   };
   auto load_k = [&]() {
     if (whole) {
-      const uint8_t* src = base_k + (size_t)(row + (uint32_t)g) * D;
+      const uint8_t* const half[2] = {base_k + (size_t)(row + (uint32_t)g) * D, base_k + (size_t)(row2 + (uint32_t)g) * D};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int q = 0; q < KQ; ++q) kr[i][q] = load_codes16(src + i * 8 * D + q * 64);
+        for (int q = 0; q < KQ; ++q) kr[i][q] = load_codes16(half[i >> 1] + (i & 1) * 8 * D + q * 64);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // rows of slot i, row group g
@@ -664,10 +668,10 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
     }
   };
   auto load_v = [&]() {
-    const uint8_t* first = base_v + (size_t)(row + 2u * (uint32_t)c) * D;
+    const uint8_t* const half[2] = {base_v + (size_t)(row + 2u * (uint32_t)c) * D, base_v + (size_t)(row2 + 2u * (uint32_t)c) * D};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // rows of slot i / 2, row groups 2 c and 2 c + 1
-      const uint8_t* src = first + (i >> 1) * 8 * D + (i & 1) * D;
+      const uint8_t* src = half[i >> 2] + ((i >> 1) & 1) * 8 * D + (i & 1) * D;
       if (!whole) src = base_v + (size_t)__shfl_sync(0xffffffffu, row, 8 * c + 4 * (i & 1) + (i >> 1)) * D;
       if constexpr (D == 128) {
         const uint4 u = load_codes16(src);
@@ -871,7 +875,8 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
       for (int v = 0; v < VR; ++v) {
         ks[v] = ks_l, lv[v] = lv_l, meta[v] = meta_l;
         const int from = (lane & 28) | (first_slot + v);
-        if (VR > 1 && !whole) {
+        // a half of a whole tile has one scale, and a lane of two rows has them in one half
+        if (VR > 1 && (!whole || (VR == 4 && row >> p.geom.lp != row2 >> p.geom.lp))) {
           ks[v] = __shfl_sync(0xffffffffu, ks_l, from);
           lv[v] = __shfl_sync(0xffffffffu, lv_l, from);
         }

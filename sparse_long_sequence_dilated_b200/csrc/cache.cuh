@@ -283,10 +283,12 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
 // d = 128, took 650 us; this takes 460 to 490 (3.2 GB: 6.6 to 7.0 TB/s).
 //
 // Ragged stretches: W warps for each (touched page, KV head), K and then V, with
-// all of its new rows in registers, 64 numbers a lane, so that they are read once.
+// all of its new rows in registers, N times 16 numbers a lane, so that they are read once.
 // Heads are the fastest index: blocks that run together read whole rows.
-template <int D, int FMT, int W>
-__global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
+// Four blocks on an SM (64 registers), three for the largest units, whose loads need
+// no more: 199 to 178 us and 81 to 74 us for small pages, 472 to 463 for 128-token ones.
+template <int D, int FMT, int W, int N>
+__global__ void __launch_bounds__(256, W == 8 ? 3 : 4) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
   constexpr int V = D / 16;  // pieces of 16 numbers of a row
   __shared__ uint32_t s_amax[2][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -306,10 +308,10 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant_
     const __nv_bfloat16* x = p.x[z] + (long long)pr.tok * p.stride[z] + (long long)h * D;
     uint8_t* codes = p.codes[z] + (blk << p.geom.lp) * D;
     float* scale = p.scale[z] + blk;
-    uint4 u[4][2];
+    uint4 u[N][2];
     uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int k = tid + i * W * 32;
       u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
       if (k / V < rows) {
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant_
     }
     const float was = work && r0 > 0 ? *scale : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) amax = max_magnitude(max_magnitude(amax, u[i][0]), u[i][1]);
+    for (int i = 0; i < N; ++i) amax = max_magnitude(max_magnitude(amax, u[i][0]), u[i][1]);
     amax = __reduce_max_sync(0xffffffffu, amax);
     if constexpr (W > 1) {
       if (lane == 0) s_amax[z][warp] = amax;
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant_
     const float inv = poisoned ? 0.f : 1.f / now;
     if (r0 > 0 && now > was) rescale_rows<D, FMT>(codes, P, r0, r0 + rows, was * inv, tid, W * 32);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int k = tid + i * W * 32;
       if (k / V >= rows) continue;
       if (poisoned) u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);

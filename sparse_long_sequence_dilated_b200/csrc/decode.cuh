@@ -890,6 +890,14 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
       look_up();
     }
     // ---- softmax weights
+    if (MODE == kDense && !some) {  // not even a substitute's codes: they may be NaN
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[rb][nb][k] = 0.f;
+    }
     float s1[VR][NB][VE], s2[VR][NB][VE], cnt[VR][NB][VE];
     bool raise = false;
 #pragma unroll

@@ -258,6 +258,37 @@ def test_codes_behind_the_last_token_are_not_read():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,pats,wide", [(3, "dense", False), (300, "dense", False), (3, "nested", False), (300, "dense", True),
+                                         (3, "dense", True), (300, "nested", True), (300, "uneven", True)])
+@pytest.mark.parametrize("H", [2, 8, 16, 32])
+def test_empty_slots_over_a_cache_that_holds_nothing(T, pats, wide, H):
+    """Codes and scales that nothing has written (NaN all of them) do not reach slots without rows,
+    nor a token whose pages are elsewhere."""
+    cache = dilattn.new_cache(40, 2, 16, 64, "e4m3")
+    for t in cache:
+        t.view(torch.uint8).fill_(0xff)
+    table = np.full((2, 1200 if wide else 4), -1)
+    q = bf16(np.random.default_rng(26).standard_normal((T, H, 64))).cuda()
+    pats = [(30000, 1), (30000, 2)] if pats == "nested" and wide else PATS[pats]
+    out, lse = dilattn.decode(q, cache, i32(table), i32([-1] * T), pats, seq=i32([0] * T))
+    torch.cuda.synchronize()
+    assert dilattn.device_error() == 0
+    assert (f64(out) == 0).all() and torch.isneginf(lse).all()
+    # a token with one page of finite numbers, its other page missing
+    one = torch.ones((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    table[1, 0] = 7
+    dilattn.cache_write(cache, one, one, i32(table[1:]), i32([0]))
+    out, lse = dilattn.decode(q, cache, i32(table), i32([0] + [-1] * (T - 1)), [(1 << 20, 1)], seq=i32([1] + [0] * (T - 1)))
+    torch.cuda.synchronize()
+    assert dilattn.device_error() == 0
+    assert (f64(out[0]) == 1).all() and torch.isfinite(lse[0]).all()
+    assert (f64(out[1:]) == 0).all() and torch.isneginf(lse[1:]).all()
+    out, lse = dilattn.decode(q, cache, i32(table), i32([20] * T), [(4, 1)], seq=i32([1] * T))
+    torch.cuda.synchronize()
+    assert dilattn.device_error() == 4
+    assert (f64(out) == 0).all() and torch.isneginf(lse).all()
+
+
 def test_pages_and_positions_out_of_range_are_skipped_and_reported():
     rng = np.random.default_rng(18)
     pair, table = filled(rng, [48, 48], 1, 16, 64, "int8")

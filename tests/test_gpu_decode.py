@@ -393,6 +393,60 @@ def test_a_captured_step_of_a_padded_batch():
         check_decode(got, ref.decode(c, pair.ref, table, at + [-1], [0, 1, 2, 0], pats), c, pair)
 
 
+@pytest.mark.parametrize("tokens", [2, 90])
+def test_calls_on_forked_streams_in_one_graph(tokens):
+    """K and V rows made on one stream, queries on another, joined before the write and the decode;
+    two decodes side by side afterwards, with a workspace each; memory set and copied in between."""
+    rng = np.random.default_rng(27)
+    lens, H, Hkv, d = [70, 900], 4, 2, 64
+    pair, table = filled(rng, lens, Hkv, 16, d, "int8")
+    dev_table, start = i32(table), i32([69, 899])
+    seq = i32(np.arange(tokens) % 2)
+    pos = i32(np.where(np.arange(tokens) % 2, 899, 69))
+    rows, q0 = normal(rng, 2, Hkv, d), normal(rng, tokens, H, d)
+    src_rows, src_q = bf16(rows).cuda(), bf16(q0).cuda()
+    rows_in, q_in = torch.empty_like(src_rows), torch.empty_like(src_q)
+    ws = [dilattn.decode_workspace(tokens, H, Hkv, d) for _ in range(2)]
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        cur = torch.cuda.current_stream()
+        rows_in.zero_()
+        other.wait_stream(cur)
+        with torch.cuda.stream(other):
+            q_in.copy_(src_q)
+        rows_in.copy_(src_rows)
+        cur.wait_stream(other)
+        dilattn.cache_write(pair.dev, rows_in, rows_in, dev_table, start)
+        other.wait_stream(cur)
+        with torch.cuda.stream(other):
+            b = dilattn.decode(q_in, pair.dev, dev_table, pos, PATS["nested"], seq=seq, workspace=ws[1])
+        a = dilattn.decode(q_in, pair.dev, dev_table, pos, PATS["dense"], seq=seq, workspace=ws[0])
+        cur.wait_stream(other)
+        return a, b
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            got = step()
+    torch.cuda.current_stream().wait_stream(main)
+    for t in range(3):
+        rows, q0 = normal(rng, 2, Hkv, d), normal(rng, tokens, H, d)
+        src_rows.copy_(bf16(rows))
+        src_q.copy_(bf16(q0))
+        if t == 0:  # what the pass before the capture wrote
+            first = f64(rows_in)
+            pair.ref.write(first, first, table, [69, 899])
+        g.replay()
+        pair.ref.write(rows, rows, table, [69, 899])
+        pair.check()
+        for (out, lse), pats in zip(got, ("dense", "nested")):
+            want = ref.decode(q0, pair.ref, table, f64(pos).astype(int), f64(seq).astype(int), PATS[pats])
+            check_decode((out, lse), want, q0, pair)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_the_set_together_with_the_forward(d):
     """A prompt through the full-sequence forward and into the cache; the cache read back and run

@@ -890,14 +890,6 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
       look_up();
     }
     // ---- softmax weights
-    if (MODE == kDense && !some) {  // not even a substitute's codes: they may be NaN
-#pragma unroll
-      for (int rb = 0; rb < 2; ++rb)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sc[rb][nb][k] = 0.f;
-    }
     float s1[VR][NB][VE], s2[VR][NB][VE], cnt[VR][NB][VE];
     bool raise = false;
 #pragma unroll
@@ -920,8 +912,9 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
           float s, t;
           cnt[v][nb][e] = 1.f;
           if constexpr (MODE == kDense) {
-            // a row that is not there has -infinity for its bias and finite codes and scales
-            s = fmaf(x, fac[i] * ks[v], meta[v] != 0 ? 0.f : -INFINITY);
+            // chosen, not added: a row that is not there has a product of any kind (its query or a
+            // substitute's codes may be NaN), but a finite lv
+            s = meta[v] != 0 ? x * (fac[i] * ks[v]) : -INFINITY;
             t = s + lv[v];
           } else {
             bool ok = meta[v] != 0;

@@ -99,6 +99,7 @@ struct DecodeParams {
   int pt_sh, ns_sh;
   int items;
   int group;                 // items of a group: 1, or what a block of decode_walks_kernel describes
+                             // (a multiple of kWalkThreads / lanes)
   int lanes;                 // threads that describe an item: a power of two, at least npat
   int warps;                 // warps of the grid
   int team;                  // blocks that share an item in decode_team_kernel; 0: a warp for each item
@@ -333,7 +334,7 @@ __device__ __forceinline__ long long block_scan(long long x, long long* s_warp) 
   return x + before;
 }
 
-// A block for each group of items.
+// A block for each group of items, which is whole rounds of what it describes at a time.
 __global__ void __launch_bounds__(kWalkThreads)
     decode_walks_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ long long s_warp[kWalkThreads / 32];

@@ -1337,6 +1337,14 @@ int decode_team(int items, double tiles, int d, int heads) {
   return tiles <= 16 ? 0 : -1;
 }
 
+// Items of a group, `lanes` threads to an item. The plan's cluster has room for kPlanBlocks *
+// kPlanThreads groups: one item each while they last, which it describes itself; else whole rounds
+// of a block of decode_walks_kernel, so that no block describes an item of another's group.
+int decode_group(long long items, int lanes) {
+  const long long most = (long long)kPlanBlocks * kPlanThreads, round = kWalkThreads / lanes;
+  return items <= most ? 1 : (int)(round * ((items + round * most - 1) / (round * most)));
+}
+
 // Workspace of a decode: the items' walks, the warps' ranges, and the partials of cut items.
 struct DecodeScratch {
   size_t head, walk, upto, sums, range, part;
@@ -1528,12 +1536,9 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   divisor_magic((uint32_t)p.per_token, p.pt_mul, p.pt_sh);
   divisor_magic((uint32_t)p.nsub, p.ns_mul, p.ns_sh);
   p.items = (int)decode_items(T, Hkv, p.G, grouped);
-  // the plan's cluster has room for kPlanBlocks * kPlanThreads groups: one item each while they
-  // last, which it describes itself, else a block's worth each
-  constexpr long long most = (long long)kPlanBlocks * kPlanThreads;
-  p.group = p.items <= most ? 1 : 64 * (int)((p.items + 64 * most - 1) / (64 * most));
   p.lanes = 1;
   while (p.lanes < p.npat) p.lanes *= 2;
+  p.group = decode_group(p.items, p.lanes);
   const DecodeScratch lay = decode_scratch(T, H, Hkv, d, grouped);
   char* at = reinterpret_cast<char*>(workspace);
   auto take = [&at](size_t n) { return at += n, at - n; };

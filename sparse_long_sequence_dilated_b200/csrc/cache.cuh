@@ -142,13 +142,11 @@ __device__ __forceinline__ PageRows page_rows(const CacheGeom& g, const CacheTok
     token_range(t, b, off, n);
     start = t.start[b];
   }
-  const bool good = start >= 0 && start <= 0x7fffffff - n;
-  if (!good) start = 0;
   const long long skip = slot - (t.offsets != nullptr ? (off >> g.lp) + 2ll * b : b);
-  const long long row0 = ((long long)(start >> g.lp) + skip) << g.lp;
+  const long long row0 = ((long long)(start >> g.lp) + skip) * P;  // below 0 as a whole, or not at all
   const long long lo = max((long long)start, row0), hi = min((long long)start + n, row0 + P);
   if (n == 0 || lo >= hi) return pr;
-  if (good) pr.page = page_of(g, b, (int)lo);
+  if (lo >= 0 && lo <= 0x7fffffff) pr.page = page_of(g, b, (int)lo);
   else g.err.raise(kErrBadPage);
   pr.r0 = (int)(lo - row0);
   pr.rows = (int)(hi - lo);

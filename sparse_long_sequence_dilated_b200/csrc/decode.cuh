@@ -720,8 +720,9 @@ __device__ __forceinline__ void decode_range(const DecodeParams& p, const Decode
       }
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      // exponent of the largest; subnormal and zero count as the smallest normal one
-      const int e = max((int)(big >> 7), 1) - 127;
+      // exponent of the largest, from -96 on: every bf16 number is a multiple of 2^-133, which the
+      // lift by 2^109 takes to fp16's smallest, and its inverse times qk_scale stays a normal number
+      const int e = max((int)(big >> 7) - 127, -96);
       // 2^(13 - e) in two factors that fp32 holds
       const int up = 13 - e, u1 = up / 2, u2 = up - u1;
       const float f1 = __uint_as_float((uint32_t)(u1 + 127) << 23), f2 = __uint_as_float((uint32_t)(u2 + 127) << 23);

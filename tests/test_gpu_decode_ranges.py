@@ -51,3 +51,25 @@ def test_queries_of_empty_slots_may_hold_anything(d, G, pats):
     assert dilattn.device_error() == 4
     check_decode((out[:2], lse[:2]), want, q[:2], pair)
     assert (f64(out[2:]) == 0).all() and torch.isneginf(lse[2:]).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_tiny_queries_over_large_keys(wide, fmt):
+    """Queries down to bf16's smallest numbers over keys up to its largest: scores near one, which
+    fp32 holds as well as those of ordinary sizes."""
+    rng = np.random.default_rng(41)
+    e = 120 if fmt == "e4m3" else 124
+    table, pages = tables(rng, [300], 16)
+    pair = Pair(pages, 1, 16, 64, fmt)
+    k = f64(bf16(normal(rng, 300, 1, 64) * 2.0 ** e))
+    pair.write(k, normal(rng, 300, 1, 64), table, [0], [0, 300])
+    # the smallest step of bf16 is 2^-133: as few as six bits are left of these
+    q = f64(bf16(normal(rng, 6, 2, 64) * 2.0 ** -np.array([96, 100, 110, 118, 122, 127])[:, None, None]))
+    pos, seq = [299, 298, 200, 17, 15, 3], [0] * 6
+    dev_table = widened(table, 6) if wide else table
+    for pats in (DENSE, SPREAD):
+        out, lse = dilattn.decode(bf16(q).cuda(), pair.dev, i32(dev_table), i32(pos), pats, seq=i32(seq))
+        torch.cuda.synchronize()
+        assert dilattn.device_error() == 0
+        check_decode((out, lse), ref.decode(q, pair.ref, table, pos, seq, pats), q, pair)

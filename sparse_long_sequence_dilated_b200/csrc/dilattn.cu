@@ -1345,6 +1345,50 @@ int decode_group(long long items, int lanes) {
   return items <= most ? 1 : (int)(round * ((items + round * most - 1) / (round * most)));
 }
 
+// The kernels that a call takes, and how they share its items.
+struct DecodeRoute {
+  int team;                // blocks of a team in decode_team_kernel; 0: a warp for each item; -1: ranges
+  bool dense;              // one pattern with r = 1
+  bool grouped;            // several tokens to an item
+  int walks;               // of an item: patterns, or tokens
+  int heads, tokens, nsub, items, group, lanes, warps;  // as in DecodeParams
+  bool plan_alone;         // the plan is one block
+  bool join_items;         // the join has a block for each item
+};
+// `longest`: positions that the table has; of_seq: tokens name their sequences.
+DecodeRoute decode_route(int T, int B, int Hkv, int G, int d, bool of_seq, const int* w, const int* r,
+                         int npat, long long longest, int num_sms) {
+  DecodeRoute a;
+  a.dense = npat == 1 && r[0] == 1;
+  // the most tiles that an item of one token can have, as far as the table goes
+  double tiles = 0;
+  for (int i = 0; i < npat; ++i) {
+    const long long n = (std::min<long long>(w[i], longest) + r[i] - 1) / r[i];
+    tiles += (double)((n + kDecTile - 1) / kDecTile);
+  }
+  a.team = decode_team((int)decode_items(T, Hkv, G, false), tiles, d, decode_heads(G, false));
+  // more tokens than sequences: several of a sequence, which attention over all that it holds (one
+  // segment) takes together; while the weights of eight contexts fit an int
+  a.grouped = a.team < 0 && a.dense && w[0] >= longest && of_seq && T > B && G <= 8 && longest < (1ll << 28);
+  a.tokens = decode_tokens(G, a.grouped);
+  a.walks = a.grouped ? a.tokens : npat;
+  a.heads = decode_heads(G, a.grouped);
+  a.nsub = a.grouped ? 1 : (G + a.heads - 1) / a.heads;
+  a.items = (int)decode_items(T, Hkv, G, a.grouped);
+  a.lanes = 1;
+  while (a.lanes < a.walks) a.lanes *= 2;
+  a.group = decode_group(a.items, a.lanes);
+  // no more warps than have work
+  const int blocks = std::min(num_sms, kDecMaxSms) * decode_blocks_per_sm(d, a.heads, a.grouped);
+  a.warps = kDecWarps * (int)std::min<double>(blocks, std::max(tiles * a.tokens, 1.0) * a.items * kSpreadWeight /
+                                                              (kDecWarps * kRangeWeight) + 1);
+  // one block saves the cluster's barriers as long as it describes all items at once
+  a.plan_alone = a.group == 1 && a.items <= kPlanAlone / a.lanes;
+  // a block for each item while they are fewer than blocks for every eight ranges
+  a.join_items = a.items <= (a.warps + kJoinWarps - 1) / kJoinWarps;
+  return a;
+}
+
 // Workspace of a decode: the items' walks, the warps' ranges, and the partials of cut items.
 struct DecodeScratch {
   size_t head, walk, upto, sums, range, part;
@@ -1365,7 +1409,7 @@ DecodeScratch decode_scratch(int T, int H, int Hkv, int d, bool grouped) {
 }
 
 template <int D, int HEADS, int FMT>
-cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
+cudaError_t launch_decode(const DecodeParams& p, const DecodeRoute& a, cudaStream_t stream) {
   if (p.team >= 0) {
     const auto kernel = decode_team_kernel<D, HEADS, FMT>;
     const size_t smem = p.team == 0 ? 0 : (size_t)(kTeamWarps + 1) * p.part_stride * 4;
@@ -1384,8 +1428,7 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
   if (p.group > 1)
     e = launch_overlapped(decode_walks_kernel, dim3((unsigned)groups), kWalkThreads, 0, stream, 1, p);
   if (e == cudaSuccess)
-    // one block saves the cluster's barriers as long as it describes all items at once
-    e = groups <= kPlanAlone / p.lanes && p.group == 1
+    e = a.plan_alone
             ? launch_overlapped(decode_plan_kernel<1>, dim3(1), kPlanAlone, 0, stream, 1, p)
             : launch_overlapped(decode_plan_kernel<kPlanBlocks>, dim3(kPlanBlocks), kPlanThreads, 0, stream,
                                 kPlanBlocks, p);
@@ -1395,21 +1438,19 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
     if (p.tokens > 1) kernel = decode_kernel<D, HEADS, FMT, kGrouped>;
   e = launch_overlapped(kernel, dim3((unsigned)(p.warps / kDecWarps)), kDecWarps * 32, 0, stream, 1, p);
   if (e != cudaSuccess) return e;
-  // a block for each item while they are fewer than blocks for every eight ranges
   const int by_ranges = (p.warps + kJoinWarps - 1) / kJoinWarps;
-  const bool few = p.items <= by_ranges;
-  return launch_overlapped(few ? decode_join_items_kernel<D> : decode_join_ranges_kernel<D>,
-                           dim3((unsigned)(few ? p.items : by_ranges), (unsigned)p.part_heads), kJoinThreads, 0, stream,
-                           1, p);
+  return launch_overlapped(a.join_items ? decode_join_items_kernel<D> : decode_join_ranges_kernel<D>,
+                           dim3((unsigned)(a.join_items ? p.items : by_ranges), (unsigned)p.part_heads), kJoinThreads,
+                           0, stream, 1, p);
 }
 template <int D, int FMT>
-cudaError_t launch_decode_heads(const DecodeParams& p, cudaStream_t stream) {
+cudaError_t launch_decode_heads(const DecodeParams& p, const DecodeRoute& a, cudaStream_t stream) {
   switch (p.heads) {
-    case 1: return launch_decode<D, 1, FMT>(p, stream);
-    case 2: return launch_decode<D, 2, FMT>(p, stream);
-    case 4: return launch_decode<D, 4, FMT>(p, stream);
-    case 8: return launch_decode<D, 8, FMT>(p, stream);
-    default: return launch_decode<D, 16, FMT>(p, stream);
+    case 1: return launch_decode<D, 1, FMT>(p, a, stream);
+    case 2: return launch_decode<D, 2, FMT>(p, a, stream);
+    case 4: return launch_decode<D, 4, FMT>(p, a, stream);
+    case 8: return launch_decode<D, 8, FMT>(p, a, stream);
+    default: return launch_decode<D, 16, FMT>(p, a, stream);
   }
 }
 
@@ -1425,8 +1466,6 @@ void decode_patterns(DecodeParams& p, const int* w, const int* r, int npat) {
   int order[kMaxPat];
   for (int i = 0; i < npat; ++i) order[i] = i;
   std::stable_sort(order, order + npat, [&](int a, int b) { return r[a] < r[b]; });
-  p.npat = npat;
-  p.dense = npat == 1 && r[0] == 1;
   for (int i = 0; i < npat; ++i) {
     p.w[i] = w[order[i]];
     p.r[i] = r[order[i]];
@@ -1511,35 +1550,25 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   p.qk_scale = (float)(1.4426950408889634 / std::sqrt((double)d));
   decode_patterns(p, w, r, npat);
   p.G = H / Hkv;
-  // the most tiles that an item of one token can have, as far as the table goes
-  const long long longest = (long long)max_pages * page_size;
-  double tiles = 0;
-  for (int i = 0; i < npat; ++i) {
-    const long long n = (std::min<long long>(w[i], longest) + r[i] - 1) / r[i];
-    tiles += (double)((n + kDecTile - 1) / kDecTile);
-  }
-  p.team = decode_team((int)decode_items(T, Hkv, p.G, false), tiles, d, decode_heads(p.G, false));
-  // more tokens than sequences: several of a sequence, which attention over all that it holds (one
-  // segment) takes together; while the weights of eight contexts fit an int
-  const bool grouped = p.team < 0 && p.dense && w[0] >= longest && seq != nullptr && T > B &&
-                       p.G <= 8 && longest < (1ll << 28);
-  p.tokens = decode_tokens(p.G, grouped);
+  const DecodeRoute a = decode_route(T, B, Hkv, p.G, d, seq != nullptr, w, r, npat,
+                                     (long long)max_pages * page_size, st->num_sms);
+  p.team = a.team;
+  p.dense = a.dense;
+  p.tokens = a.tokens;
   p.g_rec = (256 + p.G - 1) / p.G;
-  if (grouped) {
-    tiles *= p.tokens;
-    p.npat = p.tokens;
-    for (int i = 0; i < p.npat; ++i) p.r[i] = 1;
-  }
-  p.heads = decode_heads(p.G, grouped);
-  p.nsub = grouped ? 1 : (p.G + p.heads - 1) / p.heads;
+  if (a.grouped)
+    for (int i = 0; i < a.walks; ++i) p.r[i] = 1;
+  p.npat = a.walks;
+  p.heads = a.heads;
+  p.nsub = a.nsub;
   p.per_token = Hkv * p.nsub;
   divisor_magic((uint32_t)p.per_token, p.pt_mul, p.pt_sh);
   divisor_magic((uint32_t)p.nsub, p.ns_mul, p.ns_sh);
-  p.items = (int)decode_items(T, Hkv, p.G, grouped);
-  p.lanes = 1;
-  while (p.lanes < p.npat) p.lanes *= 2;
-  p.group = decode_group(p.items, p.lanes);
-  const DecodeScratch lay = decode_scratch(T, H, Hkv, d, grouped);
+  p.items = a.items;
+  p.lanes = a.lanes;
+  p.group = a.group;
+  p.warps = a.warps;
+  const DecodeScratch lay = decode_scratch(T, H, Hkv, d, a.grouped);
   char* at = reinterpret_cast<char*>(workspace);
   auto take = [&at](size_t n) { return at += n, at - n; };
   p.head = reinterpret_cast<DecodeHead*>(take(lay.head));
@@ -1548,17 +1577,13 @@ extern "C" int dilattn_decode(const void* q, long long q_stride, const void* kc,
   p.sums = reinterpret_cast<long long*>(take(lay.sums));
   p.range = reinterpret_cast<DecodeRange*>(take(lay.range));
   p.part = reinterpret_cast<float*>(take(lay.part));
-  p.part_heads = decode_columns(p.G, grouped);
+  p.part_heads = decode_columns(p.G, a.grouped);
   p.part_stride = p.part_heads * (d + 4);
-  // no more warps than have work
-  const int blocks = std::min(st->num_sms, kDecMaxSms) * decode_blocks_per_sm(d, p.heads, grouped);
-  p.warps = kDecWarps * (int)std::min<double>(blocks, std::max(tiles, 1.0) * p.items * kSpreadWeight /
-                                                              (kDecWarps * kRangeWeight) + 1);
   cudaError_t e;
   if (format == DILATTN_CACHE_E4M3)
-    e = d == 64 ? launch_decode_heads<64, kFmtE4M3>(p, stream) : launch_decode_heads<128, kFmtE4M3>(p, stream);
+    e = d == 64 ? launch_decode_heads<64, kFmtE4M3>(p, a, stream) : launch_decode_heads<128, kFmtE4M3>(p, a, stream);
   else
-    e = d == 64 ? launch_decode_heads<64, kFmtInt8>(p, stream) : launch_decode_heads<128, kFmtInt8>(p, stream);
+    e = d == 64 ? launch_decode_heads<64, kFmtInt8>(p, a, stream) : launch_decode_heads<128, kFmtInt8>(p, a, stream);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   return DILATTN_OK;
 }

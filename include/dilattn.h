@@ -304,9 +304,11 @@ int dilattn_cache_read(const void* kc, const void* vc, const float* ks, const fl
  * lse [T][H] float32, natural log, or NULL. pos[i] < 0 is an empty slot: like
  * a token that no pattern keeps it gets out = 0 and lse = -inf.
  *
- * Tokens may come in any order and share a sequence (drafted tokens: with a
- * pattern of r = 1 that holds every position, tokens of one sequence that
- * follow one another in q read the cache together).
+ * Tokens may come in any order and share a sequence. Drafted tokens, those of
+ * one sequence that follow one another in q, read the cache together under one
+ * pattern of r = 1 that holds every position of the table, with seq given,
+ * H / Hkv <= 8 and at least three tokens for every two rows of the table
+ * (where a call is too small to be split at all, each reads for itself).
  *
  * Scores, softmax and sums are fp32; q (elements below 2^-37 of its head's
  * largest aside) and the codes are exact operands, and the probabilities are

@@ -63,6 +63,9 @@ def _cases():
                     longest=70016, of_seq=False)
                 add(f"long_among-{name}-{H}-{Hkv}-{d}", dict(team=-1, join_items=0), 320, 320, H, Hkv, d, PATS[name],
                     longest=40000, of_seq=False)
+        # tokens of a sequence are taken together from one and a half a sequence on, padded slots or not
+        for T, grouped in ((32, 0), (33, 0), (47, 0), (48, 1), (128, 1)):
+            add(f"padded-{T}-{d}", dict(team=-1, grouped=grouped), T, 32, 8, 2, d, DENSE)
         # one workspace, used again and again: three tokens, and some hundred
         add(f"again-dense-3-{d}", dict(team=-1, grouped=0, dense=1, join_items=1), 3, 3, 8, 2, d, DENSE)
         add(f"again-spread-3-{d}", dict(team=-1, join_items=1), 3, 3, 8, 2, d, PATS["spread"])

@@ -266,3 +266,25 @@ def test_a_captured_step_in_ranges(pats):
         pair.ref.write(a, b, table, at)
         pair.check()
         check_decode(got, ref.decode(c, pair.ref, table, at + [-1], [0, 1, 2, 0], pats), c, pair)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("name", case("padded"))
+def test_padded_batches_and_drafts(name, fmt):
+    """A token of each of 32 sequences with padded slots, more than one of some, and four of each;
+    among them a sequence that there is not and positions past the table."""
+    c = CASES[name]
+    rng = np.random.default_rng(c["T"])
+    lens = [700] + list(rng.integers(1, 90, 31))
+    pair, table = filled(rng, lens, c["Hkv"], 16, c["d"], fmt)
+    T = c["T"]
+    seq = np.sort(np.arange(T) % 32)
+    left = np.array([np.sum(seq[i:] == seq[i]) for i in range(T)])  # drafts end at their sequence's last token
+    pos = np.array([lens[b] for b in seq]) - left
+    seq[-3:], pos[-3:], pos[5] = [31, 32, -1], [-1, 5, 5], c["longest"]
+    q = normal(rng, T, c["H"], c["d"])
+    out, lse = dilattn.decode(bf16(q).cuda(), pair.dev, i32(widened(table, 32)), i32(pos), c["pats"], seq=i32(seq))
+    torch.cuda.synchronize()
+    assert dilattn.device_error() == 4
+    pos[[5, -2, -1]], seq[-2:] = -1, 0
+    check_decode((out, lse), ref.decode(q, pair.ref, table, pos, seq, c["pats"]), q, pair)

@@ -311,8 +311,11 @@ int dilattn_cache_read(const void* kc, const void* vc, const float* ks, const fl
  * (where a call is too small to be split at all, each reads for itself).
  *
  * Scores, softmax and sums are fp32; q (elements below 2^-37 of its head's
- * largest aside) and the codes are exact operands, and the probabilities are
- * rounded to 11 bits for the product with V. The same call on the same inputs
+ * largest aside) and the codes are exact operands. For the product with V a
+ * row's probability times its V scale is rounded to 11 bits, and below 2^-21
+ * of the token and head's largest such product to a step of 2^-31 of that
+ * largest: a row whose product is under 2^-32 of it counts as zero, also in a
+ * channel that is zero in all larger rows. The same call on the same inputs
  * gives the same bits; a token's bits may depend on the other tokens of its
  * call, whose number decides how sums are split.
  *

@@ -478,7 +478,8 @@ __device__ __forceinline__ void codes_to_half(uint32_t x, uint32_t& lo, uint32_t
 constexpr float kNoMax = -3e38f;
 // Maxima are raised only when a score exceeds them by more than this (log2):
 // probabilities then reach 2^4, times at most 16 patterns; kPBias lifts them
-// to 2^15, within fp16, so that the smallest that fp16 keeps is 2^-32 of the largest.
+// to 2^15, within fp16. The largest one is then 2^7 or more, fp16's normal numbers
+// begin at 2^-14, 2^-21 of it, and its step below them is 2^-24, 2^-31 of it.
 constexpr float kMaxSlack = 4.f;
 constexpr float kPBias = 7.f;
 
@@ -509,9 +510,12 @@ __device__ __forceinline__ float final_lse(float m, float l) {
 // four), so that the softmax costs HW values a lane and not 8.
 //
 // V's scale enters through the exponent: p' = 2^(s + log2 vscale - mv) with its
-// own running maximum mv, so pages of any two sizes keep their precision, and
-// the softmax sum uses p = 2^(s - m) in fp32. p' is rounded to fp16 for the
-// product (2^-11 relative, below the bf16 rounding of the result).
+// own running maximum mv, so no page's size can overflow, and the softmax sum
+// uses p = 2^(s - m) in fp32. p' is rounded to fp16 for the product: 2^-11
+// relative, below the bf16 rounding of the result, for rows down to 2^-21 of the
+// largest p', and below that 2^-32 of the largest (see kPBias): what a row adds
+// to a channel is lost where its p' is under that, however small the larger
+// rows are in that channel.
 // ---------------------------------------------------------------------------
 
 // One warp's tiles from rg up to end. Items' heads and walks are at head[0] and

@@ -288,3 +288,39 @@ def test_padded_batches_and_drafts(name, fmt):
     assert dilattn.device_error() == 4
     pos[[5, -2, -1]], seq[-2:] = -1, 0
     check_decode((out, lse), ref.decode(q, pair.ref, table, pos, seq, c["pats"]), q, pair)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e", [0, 12, 20, 24, 33, 60])
+def test_channels_that_only_small_pages_fill(e, d, fmt, wide):
+    """Each page of V fills a channel of its own, pages 2^e apart. A row's probability times its V
+    scale, z, is rounded to 11 bits, or, below 2^-21 of the largest z, by up to 2^-32 of that: a
+    channel is off by 2^-32 max z sum |code| / sum p beside the usual bound."""
+    rng = np.random.default_rng(46)
+    table, pages = tables(rng, [64], 16)
+    pair = Pair(pages, 1, 16, d, fmt)
+    k, v = f64(bf16(normal(rng, 64, 1, d) / 8)), np.zeros((64, 1, d))
+    for page in range(4):
+        v[16 * page:16 * page + 16, 0, 9 * page] = rng.integers(1, 8, 16) * 2.0 ** (e * (page % 2) - page)
+    pair.write(k, v, table, [0], [0, 64])
+    q = normal(rng, 2, 2, d)
+    pos, seq = [63, 40], [0, 0]
+    out, lse = dilattn.decode(bf16(q).cuda(), pair.dev, i32(widened(table, 2) if wide else table), i32(pos), DENSE,
+                              seq=i32(seq))
+    torch.cuda.synchronize()
+    assert dilattn.device_error() == 0
+    want = ref.decode(q, pair.ref, table, pos, seq, DENSE)
+    if e <= 20:
+        check_decode((out, lse), want, q, pair)
+    wo, wl, spread = want
+    assert np.abs(f64(lse) - wl).max() <= 1e-4
+    for i in range(2):
+        x = np.arange(pos[i] + 1)
+        codes = np.abs(pair.ref.codes[1, table[0][x // 16], 0, x % 16])           # [rows, d]
+        scale = pair.ref.scale[1, table[0][x // 16], 0]
+        for h in range(2):
+            p = np.exp(pair.ref.rows(0, table[0], x)[:, 0] @ q[i, h] / np.sqrt(d) - wl[i, h])  # sums to one
+            tol = 2.0 ** -8 * np.abs(wo[i, h]) + 2.0 ** -10 * spread[i, h] + 2.0 ** -32 * (p * scale).max() * codes.sum(0)
+            assert (np.abs(f64(out[i, h]) - wo[i, h]) <= tol).all()

@@ -244,7 +244,7 @@ int dilattn_bwd(const void* q, const void* k, const void* v, const void* out,
  * (int32) names, position p in page table[b][p / page_size] at row
  * p mod page_size; entries past a sequence's last token are not read. All
  * arrays are device memory, so a captured graph follows their contents.
- * pages * Hkv * page_size < 2^32 and max_pages * page_size < 2^31.
+ * pages * Hkv * page_size < 2^32, max_pages * page_size < 2^31 and B < 2^30.
  *
  * What device memory holds is checked by the kernels: a page index that names
  * no page, a position outside the table or a sequence outside [0, B) is

@@ -1084,8 +1084,8 @@ int check_cache(const void* kc, const void* vc, const float* ks, const float* vs
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
     return DILATTN_ERR_INVALID_ARG;
   if (format != DILATTN_CACHE_E4M3 && format != DILATTN_CACHE_INT8) return DILATTN_ERR_INVALID_ARG;
-  // cache rows are counted in 32 bits, positions in 31
-  if ((double)pages * Hkv * page_size >= 4294967295.0 ||
+  // cache rows are counted in 32 bits, positions in 31, the sequences of a warp's search in 30
+  if (B >= (1 << 30) || (double)pages * Hkv * page_size >= 4294967295.0 ||
       (double)max_pages * page_size > 2147483647.0)
     return DILATTN_ERR_INVALID_ARG;
   if (!aligned16(kc) || !aligned16(vc) || !aligned16(ks) || !aligned16(vs) || !aligned4(table))

@@ -205,7 +205,8 @@ __device__ __forceinline__ void rescale_rows(uint8_t* codes, int P, int r0, int 
   }
 }
 
-// Bound by the four loads that follow one another: offsets, page, row, scale.
+// Bound by loads that follow one another: the offsets (two rounds of the search above
+// 32 sequences), the page, then its rows and scale together.
 // Few tokens of each sequence: a warp for each (touched page, KV head, K or V).
 // A page's first four new rows stay in registers, others are read twice.
 template <int D, int FMT>
@@ -276,9 +277,10 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
   if (lane == 0) *scale = now;
 }
 
-// Bound by DRAM: two bytes in and one out a number. With the page as the fastest
-// index instead of the head, and rows read twice, 131072 tokens of 32 heads,
-// d = 128, took 650 us; this takes 460 to 490 (3.2 GB: 6.6 to 7.0 TB/s).
+// Bound by DRAM: two bytes in and one out a number. 131072 tokens of 32 heads,
+// d = 128 (3.2 GB) take 527 us as a call among others (6.1 TB/s), and 490 to 498
+// replayed from a graph over inputs that lie in place (6.5 TB/s), where the page as
+// the fastest index instead of the head, and rows read twice, took 650 us.
 //
 // Ragged stretches: W warps for each (touched page, KV head), K and then V, with
 // all of its new rows in registers, N times 16 numbers a lane, so that they are read once.
@@ -374,8 +376,9 @@ __device__ __forceinline__ int sequence_of(const CacheReadParams& p, long long t
 }
 
 // Bound by DRAM: one byte in and two out a number (131072 tokens of 32 heads, d = 128:
-// 507 to 543 us, 5.9 to 6.4 TB/s). Page by page, as writes go, the rows would go
-// out in pieces of 256 bytes: 583 us.
+// 538 to 547 us as a call among others, 5.9 to 6.0 TB/s; 505 to 517 replayed from a
+// graph). Page by page, as writes go, the rows would go out in pieces of 256 bytes:
+// 583 us where this took 507.
 //
 // A block has kReadThreads * EACH successive pieces of 16 codes, in the order of the rows that
 // it writes: they are two thirds of the traffic. Two warps find the sequences of its first and

@@ -30,10 +30,11 @@
 // below the machine's balance: the cache's bytes at the copy rate are the floor,
 // and bytes under way what a warp has to keep up. mma.sync serves that: its
 // 16-row tiles fit any row list and any number of heads from one on, the tensor
-// pipe is 10 to 16% busy, and nothing has to pass through shared memory or TMEM.
-// A ring of tiles in shared memory filled by cp.async (three stages, 16 warps)
-// took 440 us where registers take 350 for 1,048,576 tokens of 8 KV heads with
-// 4 query heads each, d = 128 (2.1 GB: 6.1 TB/s).
+// pipe is 11 to 18% busy, and nothing has to pass through shared memory or TMEM.
+// 1,048,576 tokens of 8 KV heads with 4 query heads each, d = 128 (2.1 GB), take
+// 390 us as a call among others (5.5 TB/s), and 340 to 350 replayed from a graph
+// (6.1 TB/s), where a ring of tiles in shared memory filled by cp.async (three
+// stages, 16 warps) took 440.
 //
 // Launches: few or short items have decode_team_kernel alone. Otherwise
 // decode_plan_kernel, one block or cluster, describes every item's walks once

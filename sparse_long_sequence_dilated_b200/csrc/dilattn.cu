@@ -1172,8 +1172,8 @@ cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, s
 template <int D, int FMT>
 cudaError_t launch_cache_write(const CacheWriteParams& p, long long slots, int page_size, cudaStream_t stream) {
   const long long units = slots * p.geom.Hkv;
-  // few tokens of each sequence: a warp a page, which does not idle where a page has few new rows. At
-  // 1, 8 and 16 tokens of each of 64 sequences of 32 heads it takes 5, 7 and 10 us where the other
+  // few tokens of each sequence (on average, which is all that the host knows): a warp a page, which
+  // does not idle where a page has few new rows. At 1, 8 and 16 tokens of each of 64 sequences of 32 heads it takes 5, 7 and 10 us where the other
   // takes 23, 25 and 27, of 16 sequences of 12 heads 2.7, 3.2 and 4.1 against 3.9, 3.9 and 4.0
   if (p.tok.offsets == nullptr || p.tok.T <= 8 * (long long)p.geom.B)
     return launch_overlapped(cache_append_kernel<D, FMT>, dim3((unsigned)((2 * units + 7) / 8)), 256, 0, stream, 1,

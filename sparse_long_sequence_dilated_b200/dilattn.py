@@ -574,7 +574,9 @@ def decode(q, cache: Cache, table, pos, patterns, seq=None, out=None, lse=None, 
            stream=None):
     """dilattn_decode: dilated attention of single query tokens (bf16 [T, H, d]) at positions
     pos (int32 [T]; negative: an empty slot) of sequences seq (int32 [T]; None: token i belongs
-    to sequence i) over the cached positions up to and including their own.
+    to sequence i) over the cached positions up to and including their own. The kernels are chosen
+    by the table's width, so a table much wider than the contexts costs a short call some
+    microseconds.
 
     Returns (out [T, H, d] bf16, lse [T, H] float32)."""
     if stream is None:
